@@ -28,9 +28,16 @@ from .api import (  # noqa: E402
     get_dispatch_layout_noalloc,
     get_error,
     get_sweep_rate,
+    grouped_gemm,
+    grouped_swiglu,
     ll_dispatch,
+    ll_grouped_gemm,
+    ll_grouped_swiglu,
     ll_reset,
     ll_size_hint,
+    moe_decode,
+    moe_decode_workspace,
+    quantize_weights,
     Received,
     recv_permute,
     scale_stride,
@@ -44,4 +51,5 @@ __all__ = ["EpxError", "Layout", "Dispatched", "LowLatency", "workspace_size", "
            "dispatch", "combine", "combine_partial", "combine_final", "ll_reset", "alloc_ll",
            "ll_dispatch", "Received", "recv_permute", "fused_workspace_size",
            "fused_launches", "dispatch_fused", "set_sweep_rate", "get_sweep_rate",
-           "calibrate_sweep_rate"]
+           "calibrate_sweep_rate", "quantize_weights", "grouped_gemm", "grouped_swiglu",
+           "ll_grouped_gemm", "ll_grouped_swiglu", "moe_decode_workspace", "moe_decode"]

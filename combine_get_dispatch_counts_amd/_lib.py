@@ -14,6 +14,7 @@ EPX_OK, EPX_EINVAL, EPX_ECAPACITY, EPX_EUNSUPPORTED, EPX_EHIP, EPX_EDEVICE = 0, 
 DEV_BAD_ROUTE, DEV_OVERFLOW, DEV_BAD_HANDLE, DEV_WORKSPACE = 1, 2, 4, 8
 MAX_TOPK, MAX_EXPERTS, MAX_RANKS, MAX_SWEEP_GBPS = 32, 512, 64, 100000
 NOALLOC_SCRATCH_BYTES = 1 << 20
+MAX_CHANNELS, MAX_DECODE_TOKENS = 65536, 64
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -45,6 +46,14 @@ SIGNATURES = {
     "epx_combine_final": (_I, [_P, _P, _I64, _I, _P, _P, _I, _I, _P, _P]),
     "epx_ll_reset": (_I, [_P, _P, _I64, _P]),
     "epx_ll_dispatch": (_I, [_P, _P, _I, _P] + [_I] * 8 + [_P] * 5 + [_P, _I64, _P, _P]),
+    "epx_quantize_weights": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
+    "epx_grouped_gemm": (_I, [_P, _P, _P, _I64, _I, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "epx_grouped_swiglu": (_I, [_P, _P, _P, _I64, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "epx_ll_grouped_gemm": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _I, _P, _P]),
+    "epx_ll_grouped_swiglu": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _I, _P, _P, _P]),
+    "epx_moe_decode_workspace": (_SZ, [_I, _I, _I]),
+    "epx_moe_decode": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _SZ, _P,
+                            _P]),
     "epx_get_error": (_I, [_P, ctypes.POINTER(_I), _P]),
 }
 

@@ -596,10 +596,200 @@ def ll_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, num_experts: int, num_r
     return buf
 
 
+def quantize_weights(w: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None
+                     ) -> tuple[torch.Tensor, torch.Tensor]:
+    """bf16 expert weights [E, N, K] (K a multiple of 128) into e4m3 codes
+    (uint8 [E, N, K]) and one fp32 scale per 128 x 128 block
+    ([E, ceil(N/128), K/128]): the weight format of grouped_gemm,
+    grouped_swiglu and moe_decode. ``out`` (codes, scales) avoids allocating."""
+    _need(w, torch.bfloat16, "w", 3)
+    dev = w.device
+    E, N, K = w.shape
+    if K % 128:
+        raise EpxError(_lib.EPX_EUNSUPPORTED, f"FP8 weights need K % 128 == 0 (K = {K})")
+    if out is None:
+        out = (torch.empty((E, N, K), dtype=torch.uint8, device=dev),
+               torch.empty((E, -(-N // 128), K // 128), dtype=torch.float32, device=dev))
+    codes, scales = out
+    _need(codes, torch.uint8, "codes", shape=(E, N, K), device=dev)
+    _need(scales, torch.float32, "scales", shape=(E, -(-N // 128), K // 128), device=dev)
+    check(_lib.load().epx_quantize_weights(_ctx(dev), _p(w), E, N, K, _p(codes), _p(scales),
+                                           _stream(dev)), "epx_quantize_weights")
+    return codes, scales
+
+
+def _grouped_operands(x, w, x_scales, w_scales, gated: bool):
+    """Dtypes and shapes of a product's operands: (device, rows, K, experts,
+    output columns, fp8)."""
+    if x is None or not x.is_cuda or x.dim() != 2:
+        raise ValueError("x must be a 2-d GPU tensor")
+    dev, fp8 = x.device, x.dtype == torch.uint8
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    _need(x, dt, "x", 2)
+    _need(w, dt, "w", 3, device=dev)
+    n, K = x.shape
+    L, rows_w, _ = w.shape
+    _need(w, dt, "w", shape=(L, rows_w, K))
+    if gated and rows_w % 2:
+        raise ValueError("w must hold the gate rows, then as many up rows")
+    if fp8:
+        _need(x_scales, torch.float32, "x_scales", shape=(n, scale_stride(K)), device=dev)
+        _need(w_scales, torch.float32, "w_scales", shape=(L, -(-rows_w // 128), K // 128),
+              device=dev)
+    elif x_scales is not None or w_scales is not None:
+        raise ValueError("scales go with FP8 operands (uint8 codes)")
+    return dev, n, K, L, rows_w // 2 if gated else rows_w, fp8
+
+
+def _swiglu_out(n: int, f: int, fp8: bool, out, out_scales, dev):
+    if out is None:
+        out = torch.empty((n, f), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
+    _need(out, torch.uint8 if fp8 else torch.bfloat16, "out", shape=(n, f), device=dev)
+    if fp8:
+        if out_scales is None:
+            out_scales = torch.empty((n, scale_stride(f)), dtype=torch.float32, device=dev)
+        _need(out_scales, torch.float32, "out_scales", shape=(n, scale_stride(f)), device=dev)
+    elif out_scales is not None:
+        raise ValueError("out_scales goes with FP8 operands (uint8 codes)")
+    return out, out_scales
+
+
+def grouped_gemm(x: torch.Tensor, w: torch.Tensor, exp_off: torch.Tensor,
+                 x_scales: torch.Tensor | None = None, w_scales: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[r] = x[r] @ w[e].T in bf16 for the rows [exp_off[e], exp_off[e+1])
+    of each expert e: x [rows, K] expert-major (dispatch's recv_x), w
+    [L, N, K], exp_off int32 [L+1] on the device. bf16 operands, or uint8 e4m3
+    codes with x_scales [rows, scale_stride(K)] (dispatch's recv_scales) and
+    w_scales [L, ceil(N/128), K/128] (quantize_weights'). Rows of no expert
+    are not written."""
+    dev, n, K, L, N, fp8 = _grouped_operands(x, w, x_scales, w_scales, False)
+    _need(exp_off, torch.int32, "exp_off", shape=(L + 1,), device=dev)
+    if out is None:
+        out = torch.empty((n, N), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", shape=(n, N), device=dev)
+    check(_lib.load().epx_grouped_gemm(_ctx(dev), _p(x), _p(x_scales), n, K, _p(w), _p(w_scales),
+                                       L, N, int(fp8), _p(exp_off), _p(out), _stream(dev)),
+          "epx_grouped_gemm")
+    return out
+
+
+def grouped_swiglu(x: torch.Tensor, w: torch.Tensor, exp_off: torch.Tensor,
+                   x_scales: torch.Tensor | None = None, w_scales: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, out_scales: torch.Tensor | None = None
+                   ) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """grouped_gemm with w [L, 2f, K] (gate rows, then up rows) and the gated
+    activation silu(gate) * up applied: (act, scales), act [rows, f] bf16 and
+    scales None, or with FP8 operands e4m3 codes and scales [rows,
+    scale_stride(f)] in dispatch's format, ready for grouped_gemm."""
+    dev, n, K, L, f, fp8 = _grouped_operands(x, w, x_scales, w_scales, True)
+    _need(exp_off, torch.int32, "exp_off", shape=(L + 1,), device=dev)
+    out, out_scales = _swiglu_out(n, f, fp8, out, out_scales, dev)
+    check(_lib.load().epx_grouped_swiglu(_ctx(dev), _p(x), _p(x_scales), n, K, _p(w),
+                                         _p(w_scales), L, f, int(fp8), _p(exp_off), _p(out),
+                                         _p(out_scales), _stream(dev)), "epx_grouped_swiglu")
+    return out, out_scales
+
+
+def _ll_regions(n: int, L: int, ll_count: torch.Tensor, cap: int, dev) -> int:
+    """Regions per expert of a low-latency buffer of n rows."""
+    _need(ll_count, torch.int32, "ll_count", 1, device=dev)
+    R_buf = ll_count.numel() // L if L else 0
+    if L < 1 or R_buf < 1 or ll_count.numel() != L * R_buf:
+        raise ValueError(f"ll_count has {ll_count.numel()} entries for {L} experts")
+    if cap < 1 or n != L * R_buf * cap:
+        raise ValueError(f"x has {n} rows, the regions {L * R_buf} x {cap}")
+    return R_buf
+
+
+def ll_grouped_gemm(x: torch.Tensor, w: torch.Tensor, ll_count: torch.Tensor, cap: int,
+                    x_scales: torch.Tensor | None = None, w_scales: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """grouped_gemm over low-latency regions: x [L*R_buf*cap, K] (ll_dispatch's
+    ll_x), ll_count int32 [L*R_buf] on the device (negative: none), of which
+    R_buf consecutive regions belong to each expert. Rows past a region's
+    count are neither read nor written."""
+    dev, n, K, L, N, fp8 = _grouped_operands(x, w, x_scales, w_scales, False)
+    R_buf = _ll_regions(n, L, ll_count, cap, dev)
+    if out is None:
+        out = torch.empty((n, N), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", shape=(n, N), device=dev)
+    check(_lib.load().epx_ll_grouped_gemm(_ctx(dev), _p(x), _p(x_scales), K, _p(w), _p(w_scales),
+                                          L, N, int(fp8), _p(ll_count), R_buf, cap, _p(out),
+                                          _stream(dev)), "epx_ll_grouped_gemm")
+    return out
+
+
+def ll_grouped_swiglu(x: torch.Tensor, w: torch.Tensor, ll_count: torch.Tensor, cap: int,
+                      x_scales: torch.Tensor | None = None,
+                      w_scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      out_scales: torch.Tensor | None = None
+                      ) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """grouped_swiglu over low-latency regions (see ll_grouped_gemm)."""
+    dev, n, K, L, f, fp8 = _grouped_operands(x, w, x_scales, w_scales, True)
+    R_buf = _ll_regions(n, L, ll_count, cap, dev)
+    out, out_scales = _swiglu_out(n, f, fp8, out, out_scales, dev)
+    check(_lib.load().epx_ll_grouped_swiglu(_ctx(dev), _p(x), _p(x_scales), K, _p(w),
+                                            _p(w_scales), L, f, int(fp8), _p(ll_count), R_buf,
+                                            cap, _p(out), _p(out_scales), _stream(dev)),
+          "epx_ll_grouped_swiglu")
+    return out, out_scales
+
+
+def moe_decode_workspace(T: int, K: int, f: int) -> int:
+    return int(_lib.load().epx_moe_decode_workspace(T, K, f))
+
+
+def moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+               w13: torch.Tensor, w2: torch.Tensor, w13_scales: torch.Tensor | None = None,
+               w2_scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The whole expert layer for up to 64 tokens, in two launches: out[t] =
+    sum over k of topk_weights[t,k] * w2[e] (silu(gate) * up), e =
+    topk_idx[t,k] (-1: none), gate and up the halves of w13[e] x[t]. x [T,h]
+    bf16; w13 [E,2f,h] and w2 [E,h,f] bf16, or uint8 e4m3 codes with
+    quantize_weights' scales. ``workspace`` (moe_decode_workspace(T, K, f)
+    bytes; calls that share one must not overlap) and ``out`` avoid
+    allocating."""
+    _need(x, torch.bfloat16, "x", 2)
+    dev = x.device
+    T, h = x.shape
+    _need(topk_idx, torch.int64, "topk_idx", 2, device=dev)
+    K = topk_idx.shape[1]
+    _need(topk_idx, torch.int64, "topk_idx", shape=(T, K))
+    _need(topk_weights, torch.float32, "topk_weights", shape=(T, K), device=dev)
+    fp8 = w13 is not None and w13.dtype == torch.uint8
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    _need(w13, dt, "w13", 3, device=dev)
+    E, f = w13.shape[0], w13.shape[1] // 2
+    _need(w13, dt, "w13", shape=(E, 2 * f, h))
+    _need(w2, dt, "w2", shape=(E, h, f), device=dev)
+    if fp8:
+        _need(w13_scales, torch.float32, "w13_scales", shape=(E, -(-2 * f // 128), h // 128),
+              device=dev)
+        _need(w2_scales, torch.float32, "w2_scales", shape=(E, -(-h // 128), f // 128),
+              device=dev)
+    elif w13_scales is not None or w2_scales is not None:
+        raise ValueError("scales go with FP8 weights (uint8 codes)")
+    if out is None:
+        out = torch.empty((T, h), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", shape=(T, h), device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(moe_decode_workspace(T, K, f), 16), dtype=torch.uint8,
+                                device=dev)
+    ws_bytes = _nbytes(workspace, dev)
+    check(_lib.load().epx_moe_decode(_ctx(dev), _p(x), h, _p(topk_idx), _p(topk_weights), T, K, E,
+                                     _p(w13), _p(w13_scales), _p(w2), _p(w2_scales), f, int(fp8),
+                                     _p(workspace), ws_bytes, _p(out), _stream(dev)),
+          "epx_moe_decode")
+    return out
+
+
 __all__ = ["EpxError", "Layout", "Dispatched", "LowLatency", "workspace_size", "ll_size_hint",
            "scale_stride", "get_error", "alloc_layout", "get_dispatch_layout", "alloc_dispatch",
            "get_dispatch_layout_noalloc", "dispatch", "combine", "combine_partial",
            "combine_final", "ll_reset", "alloc_ll",
            "ll_dispatch", "Received", "recv_permute", "fused_workspace_size",
            "fused_launches", "dispatch_fused", "set_sweep_rate", "get_sweep_rate",
-           "calibrate_sweep_rate"]
+           "calibrate_sweep_rate", "quantize_weights", "grouped_gemm", "grouped_swiglu",
+           "ll_grouped_gemm", "ll_grouped_swiglu", "moe_decode_workspace", "moe_decode"]

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libepx.so")
-SOURCES = ["epx_api.hip", "layout.hip", "dispatch.hip", "combine.hip", "fused.hip"]
+SOURCES = ["epx_api.hip", "layout.hip", "dispatch.hip", "combine.hip", "fused.hip",
+           "quantize.hip", "grouped.hip", "moe_decode.hip"]
 ARCH = "gfx950"
 
 

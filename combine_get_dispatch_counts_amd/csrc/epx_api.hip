@@ -12,6 +12,7 @@
 
 #include "epx.h"
 #include "epx_internal.h"
+#include "experts_internal.h"
 
 namespace {
 
@@ -671,6 +672,158 @@ int epx_ll_dispatch(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_
     a.pos_ll = pos_ll; a.err = ctx->d_err;
     a.clear_count = next_ll_count; a.n_clear = n_next; a.stats = ll_stats;
     return launched(epx::launch_ll_dispatch(a, fp8 != 0, stream));
+}
+
+// Checks the products' common arguments and packs them; N: output columns.
+static int grouped_args(epx_ctx *ctx, const void *x, const float *x_scales, int64_t n_rows, int K,
+                        const void *w, const float *w_scales, int L, int N, int fp8, bool gated,
+                        void *out, float *out_scales, epx::GroupedArgs &a)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if (n_rows < 0 || n_rows > INT32_MAX || L < 1 || L > EPX_MAX_EXPERTS ||
+        K > EPX_MAX_CHANNELS || N > EPX_MAX_CHANNELS)
+        return EPX_EINVAL;
+    if ((rc = check_hidden(K, fp8)) != EPX_OK || (rc = check_hidden(N, gated && fp8)) != EPX_OK)
+        return rc;
+    if (n_rows > 0) {
+        if (!x || !w || !out || (fp8 && (!x_scales || !w_scales || (gated && !out_scales))))
+            return EPX_EINVAL;
+        if (!aligned16(x) || !aligned16(w) || !aligned16(out) ||
+            (fp8 && (!aligned16(x_scales) || !aligned16(w_scales) ||
+                     (gated && !aligned16(out_scales)))))
+            return EPX_EINVAL;
+    }
+    a = epx::GroupedArgs{};
+    a.x = x; a.xs = x_scales; a.w = w; a.ws = w_scales;
+    a.n_rows = n_rows; a.K = K; a.N = N; a.L = L;
+    a.out = out; a.out_s = out_scales; a.err = ctx->d_err; a.cus = ctx->cus;
+    return EPX_OK;
+}
+
+static int grouped(epx_ctx *ctx, const void *x, const float *x_scales, int64_t n_rows, int K,
+                   const void *w, const float *w_scales, int L, int N, int fp8, bool gated,
+                   const int32_t *off, void *out, float *out_scales, hipStream_t stream)
+{
+    epx::GroupedArgs a;
+    const int rc = grouped_args(ctx, x, x_scales, n_rows, K, w, w_scales, L, N, fp8, gated, out,
+                                out_scales, a);
+    if (rc != EPX_OK)
+        return rc;
+    if (n_rows > 0 && !off)
+        return EPX_EINVAL;
+    a.off = off;
+    return launched(epx::launch_grouped(a, fp8 != 0, gated, stream));
+}
+
+static int ll_grouped(epx_ctx *ctx, const void *x, const float *x_scales, int K, const void *w,
+                      const float *w_scales, int L, int N, int fp8, bool gated,
+                      const int32_t *ll_count, int R_buf, int cap, void *out, float *out_scales,
+                      hipStream_t stream)
+{
+    if (R_buf < 1 || R_buf > EPX_MAX_RANKS || cap < 1 || L < 1 || L > EPX_MAX_EXPERTS ||
+        (int64_t)L * R_buf * cap > INT32_MAX || !ll_count)
+        return EPX_EINVAL;
+    epx::GroupedArgs a;
+    const int rc = grouped_args(ctx, x, x_scales, (int64_t)L * R_buf * cap, K, w, w_scales, L, N,
+                                fp8, gated, out, out_scales, a);
+    if (rc != EPX_OK)
+        return rc;
+    a.counts = ll_count; a.R_buf = R_buf; a.cap = cap;
+    return launched(epx::launch_grouped(a, fp8 != 0, gated, stream));
+}
+
+int epx_quantize_weights(epx_ctx *ctx, const uint16_t *w, int E, int N, int K, uint8_t *codes,
+                         float *scales, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if (E < 0 || N < 0 || E > EPX_MAX_EXPERTS || N > 2 * EPX_MAX_CHANNELS || K > EPX_MAX_CHANNELS)
+        return EPX_EINVAL;
+    if ((rc = check_hidden(K, 1)) != EPX_OK)
+        return rc;
+    if (E > 0 && N > 0 && (!w || !codes || !scales || !aligned16(w) || !aligned16(codes)))
+        return EPX_EINVAL;
+    epx::QuantizeArgs a{};
+    a.w = w; a.E = E; a.N = N; a.K = K; a.codes = codes; a.scales = scales;
+    return launched(epx::launch_quantize_weights(a, stream));
+}
+
+int epx_grouped_gemm(epx_ctx *ctx, const void *x, const float *x_scales, int64_t n_rows, int K,
+                     const void *w, const float *w_scales, int L, int N, int fp8,
+                     const int32_t *off, uint16_t *out, hipStream_t stream)
+{
+    return grouped(ctx, x, x_scales, n_rows, K, w, w_scales, L, N, fp8, false, off, out, nullptr,
+                   stream);
+}
+
+int epx_grouped_swiglu(epx_ctx *ctx, const void *x, const float *x_scales, int64_t n_rows, int K,
+                       const void *w, const float *w_scales, int L, int f, int fp8,
+                       const int32_t *off, void *out, float *out_scales, hipStream_t stream)
+{
+    return grouped(ctx, x, x_scales, n_rows, K, w, w_scales, L, f, fp8, true, off, out, out_scales,
+                   stream);
+}
+
+int epx_ll_grouped_gemm(epx_ctx *ctx, const void *x, const float *x_scales, int K, const void *w,
+                        const float *w_scales, int L, int N, int fp8, const int32_t *ll_count,
+                        int R_buf, int cap, uint16_t *out, hipStream_t stream)
+{
+    return ll_grouped(ctx, x, x_scales, K, w, w_scales, L, N, fp8, false, ll_count, R_buf, cap,
+                      out, nullptr, stream);
+}
+
+int epx_ll_grouped_swiglu(epx_ctx *ctx, const void *x, const float *x_scales, int K,
+                          const void *w, const float *w_scales, int L, int f, int fp8,
+                          const int32_t *ll_count, int R_buf, int cap, void *out,
+                          float *out_scales, hipStream_t stream)
+{
+    return ll_grouped(ctx, x, x_scales, K, w, w_scales, L, f, fp8, true, ll_count, R_buf, cap, out,
+                      out_scales, stream);
+}
+
+size_t epx_moe_decode_workspace(int T, int K, int f)
+{
+    if (T < 0 || T > EPX_MAX_DECODE_TOKENS || K < 1 || K > EPX_MAX_TOPK || f > EPX_MAX_CHANNELS ||
+        check_hidden(f, 0) != EPX_OK)
+        return 0;
+    return (size_t)T * K * f * sizeof(uint16_t);
+}
+
+int epx_moe_decode(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_idx,
+                   const float *topk_w, int T, int K, int E, const void *w13,
+                   const float *w13_scales, const void *w2, const float *w2_scales, int f,
+                   int fp8, void *ws, size_t ws_bytes, uint16_t *out, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if ((rc = check_routing(T, K, E, 1)) != EPX_OK)
+        return rc;
+    if (h > EPX_MAX_CHANNELS || f > EPX_MAX_CHANNELS)
+        return EPX_EINVAL;
+    if ((rc = check_hidden(h, fp8)) != EPX_OK || (rc = check_hidden(f, fp8)) != EPX_OK)
+        return rc;
+    if (T > EPX_MAX_DECODE_TOKENS)
+        return EPX_ECAPACITY;
+    if (T > 0) {
+        if (!x || !topk_idx || !topk_w || !w13 || !w2 || !out || !ws ||
+            (fp8 && (!w13_scales || !w2_scales)))
+            return EPX_EINVAL;
+        if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(out) ||
+            !aligned16(ws))
+            return EPX_EINVAL;
+        if (ws_bytes < epx_moe_decode_workspace(T, K, f))
+            return EPX_ECAPACITY;
+    }
+    epx::DecodeArgs a{};
+    a.x = x; a.idx = topk_idx; a.topw = topk_w;
+    a.w13 = w13; a.s13 = w13_scales; a.w2 = w2; a.s2 = w2_scales;
+    a.T = T; a.K = K; a.E = E; a.h = h; a.f = f;
+    a.act = static_cast<uint16_t *>(ws); a.out = out; a.err = ctx->d_err; a.cus = ctx->cus;
+    return launched(epx::launch_moe_decode(a, fp8 != 0, stream));
 }
 
 int epx_get_error(epx_ctx *ctx, int *device_flags, hipStream_t stream)

@@ -1,0 +1,92 @@
+// experts_device.h -- device helpers shared by the experts' products (gfx950):
+// which rows an expert has, matrix operands and the gated activation.
+//
+// Both products are computed as D = W X^T with 16 x 16 matrix instructions:
+// the weights are the A operand, so a lane's four results are four
+// consecutive output columns of ONE row (its lane % 16): a row's scale is one
+// multiply per lane, and a store takes four columns at once. The channel
+// order inside an operand is free as long as both sides use the same one.
+#pragma once
+
+#include "experts_internal.h"
+#include "fp8_device.h"
+
+namespace epx {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// 128 channels of FP8 (32 bytes a lane).
+__device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b, f32x4 c)
+{
+    // scale operands of constant 0 select the unscaled instruction
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// 32 channels of bf16 (16 bytes a lane).
+__device__ __forceinline__ f32x4 mfma_bf16(i32x4 a, i32x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b)
+{
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// silu(g) * u = g / (1 + exp(-g)) * u in fp32. exp as 2^(-g log2 e) and the
+// reciprocal are the hardware's, each within an ulp: a few 1e-7 relative,
+// far below the bf16 or e4m3 rounding that follows. exp overflows to
+// infinity for g below -88, where the quotient is zero.
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
+// Rows of expert e: the first one and how many, kept inside the caller's
+// buffer (bad: the offsets or counts say otherwise).
+__device__ __forceinline__ int expert_rows(const GroupedArgs &a, int e, int64_t &first, bool &bad)
+{
+    bad = false;
+    if (a.off) {
+        const int64_t lo = a.off[e], hi = a.off[e + 1];
+        int64_t b = lo < 0 ? 0 : lo, t = hi;
+        if (b > a.n_rows)
+            b = a.n_rows;
+        if (t > a.n_rows)
+            t = a.n_rows;
+        if (t < b)
+            t = b;
+        bad = b != lo || t != hi;
+        first = b;
+        return (int)(t - b);
+    }
+    first = (int64_t)e * a.R_buf * a.cap;
+    int n = 0;
+    for (int s = 0; s < a.R_buf; ++s) {
+        const int c = a.counts[(int64_t)e * a.R_buf + s];
+        bad |= c > a.cap;
+        n += min(max(c, 0), a.cap);
+    }
+    return n;
+}
+
+// Row number i of expert e, counted from the expert's first row.
+__device__ __forceinline__ int expert_row(const GroupedArgs &a, int e, int i)
+{
+    if (a.off)
+        return i;
+    for (int s = 0; s < a.R_buf; ++s) {
+        const int c = min(max(a.counts[(int64_t)e * a.R_buf + s], 0), a.cap);
+        if (i < c)
+            return s * a.cap + i;
+        i -= c;
+    }
+    return 0;  // not reached for i < expert_rows(e)
+}
+
+}  // namespace epx

@@ -56,7 +56,8 @@ extern "C" {
 
 /* Bits of the device error word */
 #define EPX_DEV_BAD_ROUTE 1   /* a top-k entry outside [-1, E) */
-#define EPX_DEV_OVERFLOW 2    /* a row index reached the caller's capacity */
+#define EPX_DEV_OVERFLOW 2    /* a row index reached the caller's capacity, or expert
+                                 offsets or region counts leave the buffer */
 #define EPX_DEV_BAD_HANDLE 4  /* a combine handle row >= n_rows */
 #define EPX_DEV_WORKSPACE 8   /* the layout workspace was not zeroed before its
                                  first use, or is shared by overlapping calls */
@@ -66,6 +67,8 @@ extern "C" {
 #define EPX_MAX_EXPERTS 512
 #define EPX_MAX_RANKS 64
 #define EPX_MAX_SWEEP_GBPS 100000
+#define EPX_MAX_CHANNELS 65536      /* K, N and f of the experts' products */
+#define EPX_MAX_DECODE_TOKENS 64    /* T of epx_moe_decode */
 #define EPX_NOALLOC_SCRATCH_BYTES (1u << 20) /* see epx_get_dispatch_layout_noalloc */
 
 typedef struct epx_ctx epx_ctx;
@@ -431,6 +434,93 @@ int epx_ll_dispatch(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_
                     void *ll_x, float *ll_scales, int32_t *ll_src, int32_t *ll_count,
                     int32_t *pos_ll, int32_t *next_ll_count, int64_t n_next,
                     int32_t *ll_stats, hipStream_t stream);
+
+/* Expert weights into the FP8 format of the products below: w [E, N, K] bf16
+ * (K a multiple of 128) into e4m3 codes [E, N, K] and one fp32 scale per
+ * 128 x 128 block, scales [E, ceil(N/128), K/128] (a last block of fewer rows
+ * covers the rows there are). Per block s = max(amax, 1e-4) / 448 and
+ * q = e4m3(w / s), with epx_dispatch's arithmetic: IEEE fp32 divisions,
+ * nearest even, amax over the magnitudes that compare, NaN quotients 0x7F.
+ * w and codes 16-byte aligned. EPX_EUNSUPPORTED if K % 128 != 0. */
+int epx_quantize_weights(epx_ctx *ctx, const uint16_t *w, int E, int N, int K, uint8_t *codes,
+                         float *scales, hipStream_t stream);
+
+/* Grouped product: each expert's rows times its weights.
+ * In:  x [n_rows, K], expert-major: rows [off[e], off[e+1]) belong to expert e
+ *      of L, off [L+1] int32 (the layout's exp_off; rows outside every
+ *      expert's range are not read). fp8 = 0: bf16 rows and bf16 weights, K a
+ *      multiple of 8. fp8 = 1: e4m3 codes with x_scales [n_rows,
+ *      epx_scale_stride(K)] as epx_dispatch writes them and weights as
+ *      epx_quantize_weights writes them, K a multiple of 128 (else
+ *      EPX_EUNSUPPORTED).
+ *      w [L, N, K] (the rows of w are the columns of the result; N a multiple
+ *      of 8), w_scales [L, ceil(N/128), K/128] (fp8; else may be NULL).
+ * Out: out [n_rows, N] bf16: out[r, n] = sum over k of x[r, k] * w[e, n, k];
+ *      FP8: sum over the 128-channel groups b of (x_scales[r, b] *
+ *      w_scales[e, n/128, b]) * (the group's sum of code products). Sums are
+ *      in fp32, rounded once to bf16, nearest even (NaN -> 0x7FC0). Rows of no
+ *      expert are left as they were. The same inputs give the same bytes.
+ * Offsets that decrease or leave [0, n_rows] set EPX_DEV_OVERFLOW and are
+ * clamped. 1 <= L <= 512, 0 <= n_rows <= 2^31 - 1, K and N at most
+ * EPX_MAX_CHANNELS. Buffers 16-byte aligned; out must not overlap an input. */
+int epx_grouped_gemm(epx_ctx *ctx, const void *x, const float *x_scales, int64_t n_rows, int K,
+                     const void *w, const float *w_scales, int L, int N, int fp8,
+                     const int32_t *off, uint16_t *out, hipStream_t stream);
+
+/* Grouped product with the gated activation as its epilogue: the first half
+ * of an expert's feed-forward network. Arguments as epx_grouped_gemm, with
+ * w [L, 2f, K]: rows 0 .. f-1 of an expert are its gate, f .. 2f-1 its up
+ * projection (w_scales [L, 2f/128, K/128] with fp8).
+ * Out: with g and u the fp32 products, a = g / (1 + exp(-g)) * u.
+ *      fp8 = 0: out [n_rows, f] bf16 (f a multiple of 8; out_scales NULL).
+ *      fp8 = 1: out [n_rows, f] e4m3 codes and out_scales [n_rows,
+ *      epx_scale_stride(f)], one scale per row and 128 columns in
+ *      epx_dispatch's format, padding written as +0.0f: what epx_grouped_gemm
+ *      reads next. f a multiple of 128 (else EPX_EUNSUPPORTED). */
+int epx_grouped_swiglu(epx_ctx *ctx, const void *x, const float *x_scales, int64_t n_rows, int K,
+                       const void *w, const float *w_scales, int L, int f, int fp8,
+                       const int32_t *off, void *out, float *out_scales, hipStream_t stream);
+
+/* The two products over low-latency regions: expert e's rows are the first
+ * ll_count[e*R_buf + s] rows of each region e*R_buf + s, s = 0 .. R_buf-1,
+ * which starts at row (e*R_buf + s) * cap of x and of out (epx_ll_dispatch's
+ * layout; the counts are read on the device, and a negative count -- nothing
+ * arrived -- is none). Rows past a region's count are neither read nor
+ * written. A count above cap sets EPX_DEV_OVERFLOW and is clamped. L * R_buf
+ * * cap must fit in int32, R_buf <= 64. */
+int epx_ll_grouped_gemm(epx_ctx *ctx, const void *x, const float *x_scales, int K, const void *w,
+                        const float *w_scales, int L, int N, int fp8, const int32_t *ll_count,
+                        int R_buf, int cap, uint16_t *out, hipStream_t stream);
+int epx_ll_grouped_swiglu(epx_ctx *ctx, const void *x, const float *x_scales, int K,
+                          const void *w, const float *w_scales, int L, int f, int fp8,
+                          const int32_t *ll_count, int R_buf, int cap, void *out,
+                          float *out_scales, hipStream_t stream);
+
+/* Workspace bytes of epx_moe_decode (host): T*K*f bf16 values. Returns 0 for
+ * bad arguments and for T = 0. */
+size_t epx_moe_decode_workspace(int T, int K, int f);
+
+/* The whole expert layer for T <= EPX_MAX_DECODE_TOKENS tokens, in two
+ * launches and without a dispatch:
+ *   out[t] = bf16( sum over k of topk_w[t,k] * (w2[e] a) ),  e = topk_idx[t,k],
+ *   a = bf16( silu(gate) * up ) of x[t] with expert e's halves of w13,
+ * entries of -1 skipped, sums in fp32 (a token without entries gets +0).
+ * In:  x [T, h] bf16; topk_idx [T, K] int64, topk_w [T, K] fp32 (as in
+ *      epx_dispatch; an index outside [-1, E) sets EPX_DEV_BAD_ROUTE and is
+ *      skipped; a repeated expert's weights add up);
+ *      fp8 = 0: w13 [E, 2f, h] and w2 [E, h, f] bf16, h and f multiples of 8;
+ *      fp8 = 1: codes with block scales as epx_quantize_weights writes them
+ *      (w13_scales [E, 2f/128, h/128], w2_scales [E, h/128, f/128]), h and f
+ *      multiples of 128 (else EPX_EUNSUPPORTED). Activations stay in bf16.
+ *      ws: epx_moe_decode_workspace bytes, 16-byte aligned, no initial
+ *      contents; calls that share it must not overlap.
+ * Out: out [T, h] bf16. The same inputs give the same bytes. T above the
+ * limit is EPX_ECAPACITY: dispatch, the grouped products and combine take
+ * any number of tokens. */
+int epx_moe_decode(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_idx,
+                   const float *topk_w, int T, int K, int E, const void *w13,
+                   const float *w13_scales, const void *w2, const float *w2_scales, int f,
+                   int fp8, void *ws, size_t ws_bytes, uint16_t *out, hipStream_t stream);
 
 /* Synchronise `stream`, return the device error word in *device_flags (host)
  * and clear it. Returns EPX_EDEVICE if any bit was set, EPX_OK otherwise. */
