@@ -44,11 +44,13 @@ struct Shape {
     static constexpr int kMF = BM / 16 / kWM;      // row fragments of a wave
     static constexpr int kALoads = BM / 8 / kWaves;  // 8-row loads of a wave and step
     static constexpr int kWLoads = kBN / 8 / kWaves;
+    static constexpr int kLoads = kALoads + kWLoads;
     static constexpr int kStage = (BM + kBN) * kRow;
     static constexpr int kScale = kFp8Rows ? (BM + kWave) * 16 : 0;  // 4 steps of scales
     static constexpr int kAmax = GATED && kFp8Rows ? kWN * BM * 4 : 0;
     static constexpr int kTiles = 2064;            // running row tiles of the experts
-    static constexpr int kLds = STAGES * (kStage + kScale) + kAmax + kTiles + 64;
+    static constexpr int kRing = STAGES + 1;       // tiles loaded and not yet finished
+    static constexpr int kLds = STAGES * (kStage + kScale) + kAmax + kTiles + 64 + kRing * 32;
 };
 
 // 64 lanes x 16 bytes from a buffer into LDS at lds (wave-uniform), lane l's
@@ -97,29 +99,42 @@ __device__ __forceinline__ void widen16(i32x4 c, i32x4 (&o)[2])
     }
 }
 
+template <int V>
+struct Const {
+    static constexpr int value = V;
+};
+
 // An output tile.
 struct Tile {
     int64_t first;  // the expert's first row
     int e, m0, rows, n0;  // rows: of this tile
 };
 
-// The operands of one wave fragment and step: 2 x 16 bytes per lane, in the
-// form the instruction takes.
+// A wave fragment of one step as it lies in LDS: 2 x 16 bytes per lane.
+struct Raw {
+    i32x4 lo, hi;
+    static __device__ __forceinline__ Raw read(const char *row, int pos)
+    {
+        return Raw{*reinterpret_cast<const i32x4 *>(row + pos),
+                   *reinterpret_cast<const i32x4 *>(row + (pos ^ 64))};
+    }
+};
+
+// The same in the form the instructions take.
 template <Mode MODE>
 struct Frag {
     i32x4 v[MODE == kWide ? 4 : 2];
-    __device__ __forceinline__ void read(const char *row, int pos)
+    Frag() = default;
+    __device__ __forceinline__ explicit Frag(const Raw &r)
     {
-        const i32x4 lo = *reinterpret_cast<const i32x4 *>(row + pos);
-        const i32x4 hi = *reinterpret_cast<const i32x4 *>(row + (pos ^ 64));
         if constexpr (MODE == kWide) {
             i32x4 t[2];
-            widen16(lo, t);
+            widen16(r.lo, t);
             v[0] = t[0], v[1] = t[1];
-            widen16(hi, t);
+            widen16(r.hi, t);
             v[2] = t[0], v[3] = t[1];
         } else {
-            v[0] = lo, v[1] = hi;
+            v[0] = r.lo, v[1] = r.hi;
         }
     }
 };
@@ -147,6 +162,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     float *const row_amax = reinterpret_cast<float *>(scales + STAGES * S::kScale);
     int *const tiles_before = reinterpret_cast<int *>(scales + STAGES * S::kScale + S::kAmax);
     int *const wave_tiles = tiles_before + S::kTiles / 4;
+    int *const ring = wave_tiles + 16;  // [kRing][8] tiles on their way
 
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
     const int g4 = lane >> 4, l16 = lane & 15;
@@ -222,14 +238,24 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     // ---- loads: the state of the tile being loaded
     Tile lt;
     int64_t lround = 0;
-    int lstep = 0, lbuf = 0, lgroup = 0;
-    bool lmore = tile_number(0) < total;
-    i32x4 xr, wr, sr, vr;  // buffers: rows, weights, row scales, weight scales
+    int lstep = steps, lbuf = 0, lgroup = 0, ltile = 0;
+    // buffers: rows, weights, row scales, weight scales
+    i32x4 xr{0, 0, 0, 0x00020000}, wr = xr, sr = xr, vr = xr;
     uint32_t xoff[S::kALoads], woff[S::kWLoads], soff = 0;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
     const int r8 = lane >> 3, c8 = lane & 7;  // a load's row and 16-byte piece
     const auto open_tile = [&](int64_t t) {
         find_tile(t, lt);
+        if (tid == 0) {
+            int *p = ring + ltile * 8;
+            p[0] = (int)(uint32_t)lt.first;
+            p[1] = (int)(lt.first >> 32);
+            p[2] = lt.e;
+            p[3] = lt.m0;
+            p[4] = lt.rows;
+            p[5] = lt.n0;
+        }
+        ltile = ltile + 1 == S::kRing ? 0 : ltile + 1;
         // base: the first row a load may name (regions: the expert's)
         const bool gather = !a.off && a.R_buf > 1;
         const int64_t base = lt.first + (gather ? 0 : lt.m0);
@@ -240,6 +266,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
             const int m = min(lr, lt.rows - 1);
             const int row = gather ? expert_row(a, lt.e, lt.m0 + m) : m;
             xoff[i] = (uint32_t)((int64_t)row * kbytes) + (uint32_t)((c8 ^ (lr & 7)) * 16);
+            if (lr >= ((lt.rows + 15) & ~15))
+                xoff[i] = kNowhere;
         }
         const int64_t wbase = (int64_t)lt.e * wrows + lt.n0;
         wr = buffer_of(static_cast<const char *>(a.w) + wbase * kbytes,
@@ -269,10 +297,20 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         }
         lstep = 0;
     };
-    // Issues the next step's loads.
-    const auto load_step = [&]() {
-        if (!lmore)
-            return;
+    // The next step's loads: begin_load, then load_piece(0 .. kLoads-1), then
+    // end_load. Behind the last tile they go on from nowhere (zeros into LDS
+    // that is not read again), so every step issues the same number.
+    uint32_t lat = 0, lkk = 0;
+    const auto begin_load = [&]() {
+        if (lstep == steps) {
+            const int64_t t = tile_number(lround++);
+            if (t < total) {
+                open_tile(t);
+            } else {
+                xr[2] = wr[2] = sr[2] = vr[2] = 0;  // empty buffers
+                lstep = 0;
+            }
+        }
         if constexpr (S::kFp8Rows) {
             if ((lstep & 3) == 0) {
                 const uint32_t at = lds0 + STAGES * S::kStage + lgroup * S::kScale;
@@ -282,34 +320,32 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                     load_lds(uniform(at + BM * 16), vr, soff, lstep * 4);
                 lgroup = lgroup + 1 == STAGES ? 0 : lgroup + 1;
             }
-        }
-        const uint32_t at = lds0 + lbuf * S::kStage;
-        const uint32_t kk = (uint32_t)lstep * kRow;
-        const bool cut = MODE == kBf16 && tail && lstep == steps - 1;
+        } else if (tail && lstep == steps - 1) {  // a partial last step of its tile
 #pragma unroll
-        for (int i = 0; i < S::kALoads; ++i) {
-            const int r = (i * kWaves + wave) * 8;
-            if (r < lt.rows) {
-                const uint32_t o = cut && (c8 ^ r8) * 16 >= tail
-                                       ? kNowhere
-                                       : xoff[i];
-                load_lds(uniform(at + r * kRow), xr, o, kk);
+            for (int i = 0; i < S::kALoads; ++i)
+                if ((c8 ^ r8) * 16 >= tail)
+                    xoff[i] = kNowhere;
+#pragma unroll
+            for (int i = 0; i < S::kWLoads; ++i) {
+                const int lr = (wave * S::kWLoads + i) * 8 + r8;
+                if ((c8 ^ ((lr & 3) | (lr >> (GATED ? 1 : 2) & 4))) * 16 >= tail)
+                    woff[i] = kNowhere;
             }
         }
-#pragma unroll
-        for (int i = 0; i < S::kWLoads; ++i) {
-            const int r = (wave * S::kWLoads + i) * 8;
-            const int lr = r + r8, key = (lr & 3) | (lr >> (GATED ? 1 : 2) & 4);
-            const uint32_t o = cut && (c8 ^ key) * 16 >= tail ? kNowhere : woff[i];
-            load_lds(uniform(at + (BM + r) * kRow), wr, o, kk);
-        }
+        lat = lds0 + lbuf * S::kStage + wave * 1024;
+        lkk = (uint32_t)lstep * kRow;
+    };
+    const auto load_piece = [&](int i) {
+        if (i < S::kALoads)
+            load_lds(uniform(lat + i * kWaves * 1024), xr, xoff[i], lkk);
+        else
+            load_lds(uniform(lat + BM * kRow + wave * (S::kWLoads - 1) * 1024 +
+                             (i - S::kALoads) * 1024),
+                     wr, woff[i - S::kALoads], lkk);
+    };
+    const auto end_load = [&]() {
         lbuf = lbuf + 1 == STAGES ? 0 : lbuf + 1;
-        if (++lstep == steps) {
-            const int64_t t = tile_number(++lround);
-            lmore = t < total;
-            if (lmore)
-                open_tile(t);
-        }
+        ++lstep;
     };
 
     // ---- products
@@ -321,72 +357,125 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     const char *const xlane = smem + (wm * 16 + l16) * kRow;
     const char *const wlane = smem + (BM + wrow) * kRow;
 
-    if (lmore)
-        open_tile(tile_number(0));
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
-        load_step();
+    f32x4 acc[4][MF];
+    Tile o;
     int64_t round = 0;
-    int buf = 0, group = 0;
-    for (int64_t t = tile_number(0); t < total; t = tile_number(++round)) {
-        Tile o;
-        find_tile(t, o);
-        const int frags = (o.rows + 15) >> 4;                // row fragments of the tile
-        const int mf = (frags - wm + kWM - 1) / kWM;         // of this wave
-        f32x4 acc[4][MF];
+    int mf = 0, s = 0, buf = 0, group = 0, tile = 0;
+    if (tile_number(0) >= total)
+        return;
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) {
+        begin_load();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < MF; ++i)
-                acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < steps; ++s) {
-            // at most the loads of the steps after this one may be under way:
-            // kWLoads of them at least, while there is anything left to load
-            if (STAGES == 2 || !lmore)
-                wait_and_meet<0>();
-            else
-                wait_and_meet<(STAGES - 2) * S::kWLoads>();
-            load_step();
-            const char *const xb = xlane + buf * S::kStage, *const wb = wlane + buf * S::kStage;
-            Frag<MODE> w[4];
+        for (int p = 0; p < S::kLoads; ++p)
+            load_piece(p);
+        end_load();
+    }
+    for (;;) {
+        // the step to multiply has arrived when only the loads of the steps
+        // after it are under way
+        wait_and_meet<(STAGES - 2) * S::kLoads>();
+        if (s == 0) {
+            const int *p = ring + tile * 8;
+            tile = tile + 1 == S::kRing ? 0 : tile + 1;
+            o.first = (int64_t)((uint64_t)(uint32_t)uniform(p[0]) |
+                                (uint64_t)(uint32_t)uniform(p[1]) << 32);
+            o.e = uniform(p[2]), o.m0 = uniform(p[3]), o.rows = uniform(p[4]), o.n0 = uniform(p[5]);
+            mf = (((o.rows + 15) >> 4) - wm + kWM - 1) / kWM;  // fragments of this wave
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                w[j].read(wb + (GATED ? (j >> 1) * 128 + (j & 1) * 4 : j * 4) * kRow, pos);
-            float sw[2] = {0.0f, 0.0f};
-            const char *sc = scales + group * S::kScale + (s & 3) * 4;
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+                    acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        const char *const sc = scales + group * S::kScale + (s & 3) * 4;
+        const char *const xb = xlane + buf * S::kStage, *const wb = wlane + buf * S::kStage;
+        Raw x = Raw::read(xb, pos);
+        Frag<MODE> w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = Frag<MODE>(Raw::read(wb + (GATED ? (j >> 1) * 128 + (j & 1) * 4 : j * 4) * kRow,
+                                        pos));
+        float sw[2] = {0.0f, 0.0f};
+        if constexpr (S::kFp8Rows) {
+            sw[0] = *reinterpret_cast<const float *>(sc + (BM + (GATED ? 0 : wn >> 1)) * 16);
+            if (GATED)
+                sw[1] = *reinterpret_cast<const float *>(sc + (BM + 1) * 16);
+        }
+        begin_load();
+        // The wave's row fragments in two halves, the second left out where
+        // the tile has no rows for it; the next step's loads go between the
+        // first half's products. Fragment i + 1 is read while the matrix unit
+        // works on fragment i; FP8 sums are scaled and added kLag products
+        // after their own.
+        const auto half = [&](auto from, auto to, auto loads) {
+            constexpr int I0 = decltype(from)::value, I1 = decltype(to)::value;
+            constexpr int kPer = (decltype(loads)::value + I1 - I0 - 1) / (I1 - I0);
+            float sx[I1 - I0];
             if constexpr (S::kFp8Rows) {
-                sw[0] = *reinterpret_cast<const float *>(sc + (BM + (GATED ? 0 : wn >> 1)) * 16);
-                if (GATED)
-                    sw[1] = *reinterpret_cast<const float *>(sc + (BM + 1) * 16);
+#pragma unroll
+                for (int i = I0; i < I1; ++i)
+                    sx[i - I0] =
+                        *reinterpret_cast<const float *>(sc + ((i * kWM + wm) * 16 + l16) * 16);
             }
+            if (I0 > 0)
+                x = Raw::read(xb + I0 * kWM * 16 * kRow, pos);
+            constexpr int kLag = 3;
+            f32x4 d[kLag + 1];
+            const auto add = [&](int q) {
+                const int i = q >> 2, j = q & 3;
+                const float sc_ = sx[i] * sw[GATED && j >= 2];
 #pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                if (i < mf) {
-                    Frag<MODE> x;
-                    x.read(xb + i * kWM * 16 * kRow, pos);
-                    if constexpr (!S::kFp8Rows) {
+                for (int c = 0; c < 4; ++c)
+                    acc[j][I0 + i][c] =
+                        __builtin_fmaf(sc_, d[q % (kLag + 1)][c], acc[j][I0 + i][c]);
+                // keeps the sums here: moved behind the branch between the
+                // halves, they would hold their operands until then
+                asm volatile("" : "+v"(acc[j][I0 + i]));
+            };
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[j][i] = multiply<MODE>(w[j], x, acc[j][i]);
+            for (int i = I0; i < I1; ++i) {
+                Raw next = x;
+                if (i + 1 < I1)
+                    next = Raw::read(xb + (i + 1) * kWM * 16 * kRow, pos);
+                const Frag<MODE> xf(x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (S::kFp8Rows) {
+                        const int q = (i - I0) * 4 + j;
+                        d[q % (kLag + 1)] = multiply<MODE>(w[j], xf, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                        if (q >= kLag)
+                            add(q - kLag);
+                        __builtin_amdgcn_sched_barrier(0);
                     } else {
-                        const float sx = *reinterpret_cast<const float *>(
-                            sc + ((i * kWM + wm) * 16 + l16) * 16);
-                        const float s0 = sx * sw[0], s1 = GATED ? sx * sw[1] : s0;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const f32x4 d = multiply<MODE>(w[j], x, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                acc[j][i][c] =
-                                    __builtin_fmaf(j < 2 ? s0 : s1, d[c], acc[j][i][c]);
-                        }
+                        acc[j][i] = multiply<MODE>(w[j], xf, acc[j][i]);
                     }
                 }
+#pragma unroll
+                for (int p = (i - I0) * kPer; p < (i - I0 + 1) * kPer; ++p)
+                    if (p < decltype(loads)::value)
+                        load_piece(p);
+                x = next;
+                __builtin_amdgcn_sched_barrier(0);
             }
-            buf = buf + 1 == STAGES ? 0 : buf + 1;
-            if ((s & 3) == 3 || s + 1 == steps)
-                group = group + 1 == STAGES ? 0 : group + 1;
+            if constexpr (S::kFp8Rows) {
+#pragma unroll
+                for (int q = (I1 - I0) * 4 - kLag; q < (I1 - I0) * 4; ++q)
+                    add(q);
+            }
+        };
+        half(Const<0>{}, Const<(MF + 1) / 2>{}, Const<S::kLoads>{});
+        end_load();
+        if constexpr (MF > 1) {
+            if (mf > (MF + 1) / 2)
+                half(Const<(MF + 1) / 2>{}, Const<MF>{}, Const<0>{});
         }
+        buf = buf + 1 == STAGES ? 0 : buf + 1;
+        if ((s & 3) == 3 || s + 1 == steps)
+            group = group + 1 == STAGES ? 0 : group + 1;
+        if (++s < steps)
+            continue;
+        s = 0;
 
         // ---- epilogue: lane l holds consecutive columns of rows (2 i + wm) * 16 + l16
         const auto out_row = [&](int m) -> int64_t {
@@ -484,7 +573,11 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                 // (the next write of row_amax is behind the next tile's barriers)
             }
         }
+        if (tile_number(++round) >= total)
+            break;
     }
+    // no load may reach LDS after the block has given it back
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <Mode MODE, bool GATED, int BM, int STAGES>
@@ -503,7 +596,11 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
 template <Mode MODE, bool GATED>
 hipError_t pick(const GroupedArgs &a, hipStream_t stream)
 {
-    return launch<MODE, GATED, 256, 2>(a, stream);
+    if constexpr (MODE != kWide) {
+        if (a.off && a.n_rows > 128ll * a.L)
+            return launch<MODE, GATED, 256, 2>(a, stream);
+    }
+    return launch<MODE, GATED, 128, 3>(a, stream);
 }
 
 }  // namespace
