@@ -11,9 +11,9 @@
 // One persistent block of eight waves per compute unit walks over output
 // tiles of BM rows x 256 weight rows (gated: 128 gate and the 128 up rows of
 // the same columns), 128 bytes of every row per step. Both operands go from
-// memory straight into LDS (buffer loads with the LDS as destination), STAGES
-// steps deep, and the loads run ahead across tile boundaries, so the next
-// tile's first steps arrive while this tile's epilogue runs. One barrier per
+// memory straight into LDS (buffer loads with the LDS as destination), one or
+// two steps ahead and across tile boundaries, so the next tile's first steps
+// arrive while this tile's epilogue runs. One barrier per
 // step: it publishes the step's data and tells that the buffer to be loaded
 // next has been read by every wave.
 #include "experts_device.h"
@@ -37,7 +37,7 @@ constexpr int kWM = 2, kWN = 4;          // wave grid: rows x weight rows
 constexpr int kRow = 128;                // bytes of a row in LDS
 constexpr uint32_t kNowhere = 0xFFFFFF00u;  // a buffer offset past every range: reads as zero
 
-template <Mode MODE, bool GATED, int BM, int STAGES>
+template <Mode MODE, bool GATED, int BM, int XBUF, int WBUF>
 struct Shape {
     static constexpr bool kFp8Rows = MODE != kBf16;
     static constexpr int kEsize = kFp8Rows ? 1 : 2;
@@ -45,18 +45,30 @@ struct Shape {
     static constexpr int kALoads = BM / 8 / kWaves;  // 8-row loads of a wave and step
     static constexpr int kWLoads = kBN / 8 / kWaves;
     static constexpr int kLoads = kALoads + kWLoads;
-    static constexpr int kStage = (BM + kBN) * kRow;
+    static constexpr int kXStep = BM * kRow, kWStep = kBN * kRow;  // bytes of a step
+    // Loads run XA and WA steps ahead; a step is there when only these loads,
+    // issued after its own, are under way (an iteration issues rows, then weights).
+    static constexpr int XA = XBUF - 1, WA = WBUF - 1;
+    static_assert(WA >= XA && XA >= 1, "");
+    static constexpr int kUnderWay = (XA - 1) * kLoads + (WA > XA ? kWLoads : 0);
     static constexpr int kScale = kFp8Rows ? (BM + kWave) * 16 : 0;  // 4 steps of scales
     static constexpr int kAmax = GATED && kFp8Rows ? kWN * BM * 4 : 0;
     static constexpr int kTiles = 2064;            // running row tiles of the experts
-    static constexpr int kRing = STAGES + 1;       // tiles loaded and not yet finished
-    static constexpr int kLds = STAGES * (kStage + kScale) + kAmax + kTiles + 64 + kRing * 32;
+    static constexpr int kRing = WBUF + 1;         // tiles opened and not yet finished
+    static constexpr int kScaleAt = XBUF * kXStep + WBUF * kWStep;
+    static constexpr int kAmaxAt = kScaleAt + XBUF * kScale;
+    static constexpr int kTilesAt = kAmaxAt + kAmax;
+    static constexpr int kRingAt = kTilesAt + kTiles + 64;
+    static constexpr int kLds = kRingAt + kRing * 32;
 };
 
 // 64 lanes x 16 bytes from a buffer into LDS at lds (wave-uniform), lane l's
 // bytes at lds + 16 l. Not tracked by the compiler: wait with wait_loads.
 __device__ __forceinline__ void load_lds(uint32_t lds, i32x4 rsrc, uint32_t voff, uint32_t soff)
 {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        rsrc[i] = __builtin_amdgcn_readfirstlane(rsrc[i]);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                      lds),
                  "v"(voff), "s"(rsrc), "s"(soff)
@@ -123,6 +135,7 @@ struct Raw {
 // The same in the form the instructions take.
 template <Mode MODE>
 struct Frag {
+    static constexpr int kProducts = MODE == kFp8 ? 1 : MODE == kBf16 ? 2 : 4;
     i32x4 v[MODE == kWide ? 4 : 2];
     Frag() = default;
     __device__ __forceinline__ explicit Frag(const Raw &r)
@@ -139,30 +152,26 @@ struct Frag {
     }
 };
 
+// The k-th of a step's kProducts instructions for a pair of fragments.
 template <Mode MODE>
-__device__ __forceinline__ f32x4 multiply(const Frag<MODE> &w, const Frag<MODE> &x, f32x4 c)
+__device__ __forceinline__ f32x4 multiply(const Frag<MODE> &w, const Frag<MODE> &x, int k, f32x4 c)
 {
-    if constexpr (MODE == kFp8) {
+    if constexpr (MODE == kFp8)
         return mfma_fp8(join(w.v[0], w.v[1]), join(x.v[0], x.v[1]), c);
-    } else {
-#pragma unroll
-        for (int i = 0; i < (MODE == kWide ? 4 : 2); ++i)
-            c = mfma_bf16(w.v[i], x.v[i], c);
-        return c;
-    }
+    else
+        return mfma_bf16(w.v[k], x.v[k], c);
 }
 
-template <Mode MODE, bool GATED, int BM, int STAGES>
+template <Mode MODE, bool GATED, int BM, int XBUF, int WBUF>
 __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 {
-    using S = Shape<MODE, GATED, BM, STAGES>;
+    using S = Shape<MODE, GATED, BM, XBUF, WBUF>;
     constexpr int MF = S::kMF;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    char *const scales = smem + STAGES * S::kStage;
-    float *const row_amax = reinterpret_cast<float *>(scales + STAGES * S::kScale);
-    int *const tiles_before = reinterpret_cast<int *>(scales + STAGES * S::kScale + S::kAmax);
+    float *const row_amax = reinterpret_cast<float *>(smem + S::kAmaxAt);
+    int *const tiles_before = reinterpret_cast<int *>(smem + S::kTilesAt);
     int *const wave_tiles = tiles_before + S::kTiles / 4;
-    int *const ring = wave_tiles + 16;  // [kRing][8] tiles on their way
+    int *const ring = reinterpret_cast<int *>(smem + S::kRingAt);  // [kRing][8] opened tiles
 
     const int tid = threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
     const int g4 = lane >> 4, l16 = lane & 15;
@@ -235,117 +244,143 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         o.rows = min(BM, rows - o.m0);
     };
 
-    // ---- loads: the state of the tile being loaded
-    Tile lt;
-    int64_t lround = 0;
-    int lstep = steps, lbuf = 0, lgroup = 0, ltile = 0;
-    // buffers: rows, weights, row scales, weight scales
-    i32x4 xr{0, 0, 0, 0x00020000}, wr = xr, sr = xr, vr = xr;
-    uint32_t xoff[S::kALoads], woff[S::kWLoads], soff = 0;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
     const int r8 = lane >> 3, c8 = lane & 7;  // a load's row and 16-byte piece
-    const auto open_tile = [&](int64_t t) {
-        find_tile(t, lt);
-        if (tid == 0) {
-            int *p = ring + ltile * 8;
-            p[0] = (int)(uint32_t)lt.first;
-            p[1] = (int)(lt.first >> 32);
-            p[2] = lt.e;
-            p[3] = lt.m0;
-            p[4] = lt.rows;
-            p[5] = lt.n0;
-        }
-        ltile = ltile + 1 == S::kRing ? 0 : ltile + 1;
-        // base: the first row a load may name (regions: the expert's)
-        const bool gather = !a.off && a.R_buf > 1;
-        const int64_t base = lt.first + (gather ? 0 : lt.m0);
-        xr = buffer_of(static_cast<const char *>(a.x) + base * kbytes, (a.n_rows - base) * kbytes);
-#pragma unroll
-        for (int i = 0; i < S::kALoads; ++i) {
-            const int lr = (i * kWaves + wave) * 8 + r8;  // row of the tile
-            const int m = min(lr, lt.rows - 1);
-            const int row = gather ? expert_row(a, lt.e, lt.m0 + m) : m;
-            xoff[i] = (uint32_t)((int64_t)row * kbytes) + (uint32_t)((c8 ^ (lr & 7)) * 16);
-            if (lr >= ((lt.rows + 15) & ~15))
-                xoff[i] = kNowhere;
-        }
-        const int64_t wbase = (int64_t)lt.e * wrows + lt.n0;
-        wr = buffer_of(static_cast<const char *>(a.w) + wbase * kbytes,
-                       ((int64_t)a.L * wrows - wbase) * kbytes);
-#pragma unroll
-        for (int i = 0; i < S::kWLoads; ++i) {
-            const int lr = (wave * S::kWLoads + i) * 8 + r8;
-            const int col = GATED ? lr & 127 : lr;
-            const int n = min(col, a.N - 1 - lt.n0) + (GATED && lr >= 128 ? a.N : 0);
-            const int key = (lr & 3) | (lr >> (GATED ? 1 : 2) & 4);
-            woff[i] = (uint32_t)((int64_t)n * kbytes) + (uint32_t)((c8 ^ key) * 16);
-        }
-        if constexpr (S::kFp8Rows) {
-            const int st = scale_stride(a.K);
-            if (wave < BM / kWave) {
-                sr = buffer_of(a.xs + base * st, (a.n_rows - base) * st * 4);
-                const int m = min(wave * kWave + lane, lt.rows - 1);
-                const int row = gather ? expert_row(a, lt.e, lt.m0 + m) : m;
-                soff = (uint32_t)((int64_t)row * st * 4);
-            } else if (wave == BM / kWave) {
-                const int64_t sb = ((int64_t)lt.e * nb_n + (lt.n0 >> 7)) * kb_n;
-                vr = buffer_of(a.ws + sb, ((int64_t)a.L * nb_n * kb_n - sb) * 4);
-                // lane 1: the up rows' block, or the tile's second block
-                const int blk = lane == 1 ? (GATED ? a.N >> 7 : 1) : 0;
-                soff = (uint32_t)(blk * kb_n * 4);
-            }
-        }
-        lstep = 0;
-    };
-    // The next step's loads: begin_load, then load_piece(0 .. kLoads-1), then
-    // end_load. Behind the last tile they go on from nowhere (zeros into LDS
+    const bool gather = !a.off && a.R_buf > 1;
+    // Behind the last tile the loads go on from empty buffers (zeros into LDS
     // that is not read again), so every step issues the same number.
-    uint32_t lat = 0, lkk = 0;
-    const auto begin_load = [&]() {
-        if (lstep == steps) {
-            const int64_t t = tile_number(lround++);
+
+    // ---- weight loads: they open the tiles
+    Tile wt{};
+    int64_t wround = 0;
+    int wstep = steps, wbuf = 0, wtile = 0;
+    i32x4 wr{0, 0, 0, 0x00020000};
+    uint32_t woff[S::kWLoads] = {};
+    const auto wkey = [&](int lr) { return (lr & 3) | (lr >> (GATED ? 1 : 2) & 4); };
+    const auto begin_weights = [&]() {
+        if (wstep == steps) {
+            wstep = 0;
+            const int64_t t = tile_number(wround++);
             if (t < total) {
-                open_tile(t);
+                find_tile(t, wt);
+                const int64_t base = (int64_t)wt.e * wrows + wt.n0;
+                wr = buffer_of(static_cast<const char *>(a.w) + base * kbytes,
+                               ((int64_t)a.L * wrows - base) * kbytes);
+#pragma unroll
+                for (int i = 0; i < S::kWLoads; ++i) {
+                    const int lr = (wave * S::kWLoads + i) * 8 + r8;
+                    const int col = GATED ? lr & 127 : lr;
+                    const int n = min(col, a.N - 1 - wt.n0) + (GATED && lr >= 128 ? a.N : 0);
+                    woff[i] = (uint32_t)((int64_t)n * kbytes) + (uint32_t)((c8 ^ wkey(lr)) * 16);
+                }
             } else {
-                xr[2] = wr[2] = sr[2] = vr[2] = 0;  // empty buffers
-                lstep = 0;
+                wt.rows = 0;
+                wr[2] = 0;
+            }
+            if (tid == 0) {
+                int *p = ring + wtile * 8;
+                p[0] = (int)(uint32_t)wt.first;
+                p[1] = (int)(wt.first >> 32);
+                p[2] = wt.e;
+                p[3] = wt.m0;
+                p[4] = wt.rows;
+                p[5] = wt.n0;
+            }
+            wtile = wtile + 1 == S::kRing ? 0 : wtile + 1;
+        }
+        if (MODE == kBf16 && tail && wstep == steps - 1) {  // a partial last step
+#pragma unroll
+            for (int i = 0; i < S::kWLoads; ++i)
+                if ((c8 ^ wkey((wave * S::kWLoads + i) * 8 + r8)) * 16 >= tail)
+                    woff[i] = kNowhere;
+        }
+    };
+    const auto load_weights = [&](int i) {
+        load_lds(uniform(lds0 + XBUF * S::kXStep + wbuf * S::kWStep +
+                         (wave * S::kWLoads + i) * 1024),
+                 wr, woff[i], (uint32_t)wstep * kRow);
+    };
+    const auto end_weights = [&]() {
+        wbuf = wbuf + 1 == WBUF ? 0 : wbuf + 1;
+        ++wstep;
+    };
+
+    const auto ring_tile = [&](int i) {
+        const int *p = ring + i * 8;
+        Tile o;
+        o.first = (int64_t)((uint64_t)(uint32_t)uniform(p[0]) |
+                            (uint64_t)(uint32_t)uniform(p[1]) << 32);
+        o.e = uniform(p[2]), o.m0 = uniform(p[3]), o.rows = uniform(p[4]), o.n0 = uniform(p[5]);
+        return o;
+    };
+
+    // ---- row loads, with the scales of four steps at a time
+    int xstep = steps, xbuf = 0, xtile = 0, xgroup = 0;
+    i32x4 xr{0, 0, 0, 0x00020000}, sr = xr;  // rows; row scales or weight scales
+    uint32_t xoff[S::kALoads] = {}, soff = 0;
+    const auto begin_rows = [&]() {
+        if (xstep == steps) {
+            xstep = 0;
+            const Tile o = S::XA == S::WA ? wt : ring_tile(xtile);
+            xtile = xtile + 1 == S::kRing ? 0 : xtile + 1;
+            if (o.rows > 0) {
+                // base: the first row a load may name (regions: the expert's)
+                const int64_t base = o.first + (gather ? 0 : o.m0);
+                xr = buffer_of(static_cast<const char *>(a.x) + base * kbytes,
+                               (a.n_rows - base) * kbytes);
+#pragma unroll
+                for (int i = 0; i < S::kALoads; ++i) {
+                    const int lr = (i * kWaves + wave) * 8 + r8;  // row of the tile
+                    const int m = min(lr, o.rows - 1);
+                    const int row = gather ? expert_row(a, o.e, o.m0 + m) : m;
+                    xoff[i] = (uint32_t)((int64_t)row * kbytes) + (uint32_t)((c8 ^ r8) * 16);
+                    if (lr >= ((o.rows + 15) & ~15))
+                        xoff[i] = kNowhere;
+                }
+                if constexpr (S::kFp8Rows) {
+                    const int st = scale_stride(a.K);
+                    if (wave < BM / kWave) {
+                        sr = buffer_of(a.xs + base * st, (a.n_rows - base) * st * 4);
+                        const int m = min(wave * kWave + lane, o.rows - 1);
+                        const int row = gather ? expert_row(a, o.e, o.m0 + m) : m;
+                        soff = (uint32_t)((int64_t)row * st * 4);
+                    } else {
+                        const int64_t sb = ((int64_t)o.e * nb_n + (o.n0 >> 7)) * kb_n;
+                        sr = buffer_of(a.ws + sb, ((int64_t)a.L * nb_n * kb_n - sb) * 4);
+                        // lane 1: the up rows' block, or the tile's second block
+                        const int blk = lane == 1 ? (GATED ? a.N >> 7 : 1) : 0;
+                        soff = (uint32_t)(blk * kb_n * 4);
+                    }
+                }
+                // the compiler would wait for loads made here wherever their
+                // results are used, behind loads it does not know of
+                if (gather)
+                    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+            } else {
+                xr[2] = sr[2] = 0;
             }
         }
         if constexpr (S::kFp8Rows) {
-            if ((lstep & 3) == 0) {
-                const uint32_t at = lds0 + STAGES * S::kStage + lgroup * S::kScale;
-                if (wave < BM / kWave)
-                    load_lds(uniform(at + wave * 1024), sr, soff, lstep * 4);
-                else if (wave == BM / kWave)
-                    load_lds(uniform(at + BM * 16), vr, soff, lstep * 4);
-                lgroup = lgroup + 1 == STAGES ? 0 : lgroup + 1;
+            if ((xstep & 3) == 0) {
+                if (wave <= BM / kWave)
+                    load_lds(uniform(lds0 + S::kScaleAt + xgroup * S::kScale + wave * 1024), sr,
+                             soff, (uint32_t)xstep * 4);
+                xgroup = xgroup + 1 == XBUF ? 0 : xgroup + 1;
             }
-        } else if (tail && lstep == steps - 1) {  // a partial last step of its tile
+        } else if (tail && xstep == steps - 1) {
 #pragma unroll
             for (int i = 0; i < S::kALoads; ++i)
                 if ((c8 ^ r8) * 16 >= tail)
                     xoff[i] = kNowhere;
-#pragma unroll
-            for (int i = 0; i < S::kWLoads; ++i) {
-                const int lr = (wave * S::kWLoads + i) * 8 + r8;
-                if ((c8 ^ ((lr & 3) | (lr >> (GATED ? 1 : 2) & 4))) * 16 >= tail)
-                    woff[i] = kNowhere;
-            }
         }
-        lat = lds0 + lbuf * S::kStage + wave * 1024;
-        lkk = (uint32_t)lstep * kRow;
     };
-    const auto load_piece = [&](int i) {
-        if (i < S::kALoads)
-            load_lds(uniform(lat + i * kWaves * 1024), xr, xoff[i], lkk);
-        else
-            load_lds(uniform(lat + BM * kRow + wave * (S::kWLoads - 1) * 1024 +
-                             (i - S::kALoads) * 1024),
-                     wr, woff[i - S::kALoads], lkk);
+    const auto load_rows = [&](int i) {
+        load_lds(uniform(lds0 + xbuf * S::kXStep + (i * kWaves + wave) * 1024), xr, xoff[i],
+                 (uint32_t)xstep * kRow);
     };
-    const auto end_load = [&]() {
-        lbuf = lbuf + 1 == STAGES ? 0 : lbuf + 1;
-        ++lstep;
+    const auto end_rows = [&]() {
+        xbuf = xbuf + 1 == XBUF ? 0 : xbuf + 1;
+        ++xstep;
     };
 
     // ---- products
@@ -355,32 +390,34 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     // 16 (l16 / 4) + 4 j + l16 % 4 (gated: 8 (l16 / 4) + 4 j + l16 % 4)
     const int wrow = GATED ? wn * 32 + (l16 >> 2) * 8 + (l16 & 3) : wn * 64 + (l16 >> 2) * 16 + (l16 & 3);
     const char *const xlane = smem + (wm * 16 + l16) * kRow;
-    const char *const wlane = smem + (BM + wrow) * kRow;
+    const char *const wlane = smem + XBUF * S::kXStep + wrow * kRow;
 
     f32x4 acc[4][MF];
-    Tile o;
-    int64_t round = 0;
-    int mf = 0, s = 0, buf = 0, group = 0, tile = 0;
-    if (tile_number(0) >= total)
-        return;
+    Tile o{};
+    int mf = 0, s = 0, xcur = 0, wcur = 0, group = 0, tile = 0;
 #pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) {
-        begin_load();
+    for (int it = -S::WA; it < 0; ++it) {  // fill the buffers
+        meet();
+        begin_weights();
+        if (it + S::XA >= 0) {
+            begin_rows();
 #pragma unroll
-        for (int p = 0; p < S::kLoads; ++p)
-            load_piece(p);
-        end_load();
+            for (int p = 0; p < S::kALoads; ++p)
+                load_rows(p);
+            end_rows();
+        }
+#pragma unroll
+        for (int p = 0; p < S::kWLoads; ++p)
+            load_weights(p);
+        end_weights();
     }
     for (;;) {
-        // the step to multiply has arrived when only the loads of the steps
-        // after it are under way
-        wait_and_meet<(STAGES - 2) * S::kLoads>();
+        wait_and_meet<S::kUnderWay>();
         if (s == 0) {
-            const int *p = ring + tile * 8;
+            o = ring_tile(tile);
+            if (o.rows == 0)
+                break;
             tile = tile + 1 == S::kRing ? 0 : tile + 1;
-            o.first = (int64_t)((uint64_t)(uint32_t)uniform(p[0]) |
-                                (uint64_t)(uint32_t)uniform(p[1]) << 32);
-            o.e = uniform(p[2]), o.m0 = uniform(p[3]), o.rows = uniform(p[4]), o.n0 = uniform(p[5]);
             mf = (((o.rows + 15) >> 4) - wm + kWM - 1) / kWM;  // fragments of this wave
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -388,8 +425,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                 for (int i = 0; i < MF; ++i)
                     acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        const char *const sc = scales + group * S::kScale + (s & 3) * 4;
-        const char *const xb = xlane + buf * S::kStage, *const wb = wlane + buf * S::kStage;
+        const char *const sc = smem + S::kScaleAt + group * S::kScale + (s & 3) * 4;
+        const char *const xb = xlane + xcur * S::kXStep, *const wb = wlane + wcur * S::kWStep;
         Raw x = Raw::read(xb, pos);
         Frag<MODE> w[4];
 #pragma unroll
@@ -402,14 +439,14 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
             if (GATED)
                 sw[1] = *reinterpret_cast<const float *>(sc + (BM + 1) * 16);
         }
-        begin_load();
-        // The wave's row fragments in two halves, the second left out where
-        // the tile has no rows for it; the next step's loads go between the
-        // first half's products. Fragment i + 1 is read while the matrix unit
-        // works on fragment i; FP8 sums are scaled and added kLag products
-        // after their own.
-        const auto half = [&](auto from, auto to, auto loads) {
-            constexpr int I0 = decltype(from)::value, I1 = decltype(to)::value;
+        begin_weights();
+        begin_rows();
+        // The wave's row fragments two at a time, as far as the tile has rows;
+        // the next step's loads go between the first products. Fragment i + 1
+        // is read while the matrix unit works on fragment i; FP8 sums are
+        // scaled and added kLag products after their own.
+        const auto part = [&](auto from, auto count, auto loads) {
+            constexpr int I0 = decltype(from)::value, I1 = I0 + decltype(count)::value;
             constexpr int kPer = (decltype(loads)::value + I1 - I0 - 1) / (I1 - I0);
             float sx[I1 - I0];
             if constexpr (S::kFp8Rows) {
@@ -418,44 +455,64 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                     sx[i - I0] =
                         *reinterpret_cast<const float *>(sc + ((i * kWM + wm) * 16 + l16) * 16);
             }
-            if (I0 > 0)
-                x = Raw::read(xb + I0 * kWM * 16 * kRow, pos);
-            constexpr int kLag = 3;
-            f32x4 d[kLag + 1];
+            // FP8 results on their way: kPair of the four weight fragments at
+            // a time (widened codes: two chains of four products, so that no
+            // product waits for the one before it)
+            constexpr int kPair = MODE == kWide ? 2 : 1, kLag = MODE == kWide ? 2 : 3;
+            f32x4 d[kLag + kPair];
             const auto add = [&](int q) {
                 const int i = q >> 2, j = q & 3;
                 const float sc_ = sx[i] * sw[GATED && j >= 2];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    acc[j][I0 + i][c] =
-                        __builtin_fmaf(sc_, d[q % (kLag + 1)][c], acc[j][I0 + i][c]);
-                // keeps the sums here: moved behind the branch between the
-                // halves, they would hold their operands until then
-                asm volatile("" : "+v"(acc[j][I0 + i]));
+                for (int c = 0; c < 4; ++c) {
+                    float v = __builtin_fmaf(sc_, d[q % (kLag + kPair)][c], acc[j][I0 + i][c]);
+                    // keeps the sum here: moved behind a branch between the
+                    // parts, it would hold its operands until then
+                    asm volatile("" : "+v"(v));
+                    acc[j][I0 + i][c] = v;
+                }
             };
 #pragma unroll
             for (int i = I0; i < I1; ++i) {
-                Raw next = x;
-                if (i + 1 < I1)
-                    next = Raw::read(xb + (i + 1) * kWM * 16 * kRow, pos);
                 const Frag<MODE> xf(x);
+                if (i + 1 < MF)
+                    x = Raw::read(xb + (i + 1) * kWM * 16 * kRow, pos);
+                if constexpr (S::kFp8Rows) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (S::kFp8Rows) {
+                    for (int j = 0; j < 4; j += kPair) {
                         const int q = (i - I0) * 4 + j;
-                        d[q % (kLag + 1)] = multiply<MODE>(w[j], xf, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                        if (q >= kLag)
-                            add(q - kLag);
+                        f32x4 t[kPair];
+#pragma unroll
+                        for (int u = 0; u < kPair; ++u)
+                            t[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int k = 0; k < Frag<MODE>::kProducts; ++k)
+#pragma unroll
+                            for (int u = 0; u < kPair; ++u)
+                                t[u] = multiply<MODE>(w[j + u], xf, k, t[u]);
+#pragma unroll
+                        for (int u = 0; u < kPair; ++u) {
+                            d[(q + u) % (kLag + kPair)] = t[u];
+                            if (q + u >= kLag)
+                                add(q + u - kLag);
+                        }
                         __builtin_amdgcn_sched_barrier(0);
-                    } else {
-                        acc[j][i] = multiply<MODE>(w[j], xf, acc[j][i]);
                     }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < Frag<MODE>::kProducts; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[j][i] = multiply<MODE>(w[j], xf, k, acc[j][i]);
                 }
 #pragma unroll
                 for (int p = (i - I0) * kPer; p < (i - I0 + 1) * kPer; ++p)
-                    if (p < decltype(loads)::value)
-                        load_piece(p);
-                x = next;
+                    if (p < decltype(loads)::value) {
+                        if (p < S::kALoads)
+                            load_rows(p);
+                        else
+                            load_weights(p - S::kALoads);
+                    }
                 __builtin_amdgcn_sched_barrier(0);
             }
             if constexpr (S::kFp8Rows) {
@@ -464,15 +521,22 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                     add(q);
             }
         };
-        half(Const<0>{}, Const<(MF + 1) / 2>{}, Const<S::kLoads>{});
-        end_load();
-        if constexpr (MF > 1) {
-            if (mf > (MF + 1) / 2)
-                half(Const<(MF + 1) / 2>{}, Const<MF>{}, Const<0>{});
-        }
-        buf = buf + 1 == STAGES ? 0 : buf + 1;
+        part(Const<0>{}, Const<2>{}, Const<S::kLoads>{});
+        end_rows();
+        end_weights();
+        if constexpr (MF > 2)
+            if (mf > 2)
+                part(Const<2>{}, Const<2>{}, Const<0>{});
+        if constexpr (MF > 4)
+            if (mf > 4)
+                part(Const<4>{}, Const<2>{}, Const<0>{});
+        if constexpr (MF > 6)
+            if (mf > 6)
+                part(Const<6>{}, Const<2>{}, Const<0>{});
+        xcur = xcur + 1 == XBUF ? 0 : xcur + 1;
+        wcur = wcur + 1 == WBUF ? 0 : wcur + 1;
         if ((s & 3) == 3 || s + 1 == steps)
-            group = group + 1 == STAGES ? 0 : group + 1;
+            group = group + 1 == XBUF ? 0 : group + 1;
         if (++s < steps)
             continue;
         s = 0;
@@ -573,34 +637,43 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                 // (the next write of row_amax is behind the next tile's barriers)
             }
         }
-        if (tile_number(++round) >= total)
-            break;
     }
     // no load may reach LDS after the block has given it back
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-template <Mode MODE, bool GATED, int BM, int STAGES>
+template <Mode MODE, bool GATED, int BM, int XBUF, int WBUF>
 hipError_t launch(const GroupedArgs &a, hipStream_t stream)
 {
-    using S = Shape<MODE, GATED, BM, STAGES>;
+    using S = Shape<MODE, GATED, BM, XBUF, WBUF>;
     static_assert(S::kLds <= 160 * 1024, "");
-    const auto k = grouped_kernel<MODE, GATED, BM, STAGES>;
     const int64_t cols = GATED ? kBN / 2 : kBN;
     const int64_t most = (a.n_rows / BM + a.L) * ((a.N + cols - 1) / cols);  // tiles there can be
     const int64_t blocks = most < a.cus ? most : a.cus;
-    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(kThreads), S::kLds, stream, a);
+    hipLaunchKernelGGL((grouped_kernel<MODE, GATED, BM, XBUF, WBUF>), dim3((unsigned)blocks),
+                       dim3(kThreads), S::kLds, stream, a);
     return hipGetLastError();
 }
 
+// Tile height and buffers by the rows an expert has on average (regions: by
+// the rows they hold), which is all the host knows. Few rows: the weights'
+// stream decides, and three steps of both operands in LDS keep more of it
+// under way (128 regions of 4 rows, FP8 gated: 1300 us, against 1510 for 192
+// rows with two steps of rows and three of weights). Around 128 rows: one
+// tile per expert (gated FP8, 256 experts of 128 rows: 2310 us, against 2950
+// for 128-row tiles). Many: the fewest bytes per product (bf16, 3700 rows:
+// 774 us against 804; FP8, 770 rows: 500 against 514).
 template <Mode MODE, bool GATED>
 hipError_t pick(const GroupedArgs &a, hipStream_t stream)
 {
+    const int64_t per = a.n_rows / a.L;
+    if (per <= (a.off ? 96 : 128))
+        return launch<MODE, GATED, 128, 3, 3>(a, stream);
     if constexpr (MODE != kWide) {
-        if (a.off && a.n_rows > 128ll * a.L)
-            return launch<MODE, GATED, 256, 2>(a, stream);
+        if (a.off && per > 384)
+            return launch<MODE, GATED, 256, 2, 2>(a, stream);
     }
-    return launch<MODE, GATED, 128, 3>(a, stream);
+    return launch<MODE, GATED, 192, 2, 3>(a, stream);
 }
 
 }  // namespace
