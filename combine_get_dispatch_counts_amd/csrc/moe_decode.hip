@@ -11,15 +11,14 @@
 // channels; the tokens stay in bf16.
 //
 // A wave owns 16 weight rows (the A operand of D = W X^T) and a share of the
-// channels; its expert's tokens are the B operand, 16 at a time, up to all
-// 64 held as accumulators at once, so a weight is loaded once whatever the
-// number of tokens.
+// channels; its expert's tokens are the B operand, up to 32 at a time: a
+// weight is loaded once for 32 tokens of its expert.
 #include "experts_device.h"
 
 namespace epx {
 namespace {
 
-constexpr int kWaves = 4, kThreads = kWaves * kWave;
+constexpr int kUpWaves = 4, kDownWaves = 8;
 constexpr int kMaxEntries = kDecodeMaxTokens * EPX_MAX_TOPK;
 
 // Entries of the routing table grouped by expert, in LDS.
@@ -28,15 +27,17 @@ struct Groups {
     short active[EPX_MAX_EXPERTS];    // experts with entries, ascending
     short entry[kMaxEntries];         // t * K + k, expert by expert
     int n_active;
-    int part[kWaves];
+    int part[kDownWaves];
 };
 
 // Fills g. An entry whose token already has an earlier entry with the same
 // expert is left out: its weight is added to the earlier one's where the
 // weights are used. The order inside an expert's list is not fixed; nothing
 // depends on it (each list position is a column of its own).
-__device__ void group_entries(const DecodeArgs &a, Groups &g)
+template <int kWaves>
+__device__ __forceinline__ void group_entries(const DecodeArgs &a, Groups &g)
 {
+    constexpr int kThreads = kWaves * kWave;
     const int tid = threadIdx.x, n = a.T * a.K;
     for (int e = tid; e <= EPX_MAX_EXPERTS; e += kThreads)
         g.start[e] = 0;
@@ -96,9 +97,8 @@ __device__ void group_entries(const DecodeArgs &a, Groups &g)
     __syncthreads();
 }
 
-// A lane's 16 weights of a 64-channel step as two bf16 operands: channels
-// 16 (lane / 16) + 0..7 and + 8..15.
-__device__ __forceinline__ i32x4 widen(int lo, int hi)
+// Sixteen e4m3 codes (two registers' worth of each half) as bf16 operands of eight.
+__device__ __forceinline__ i32x4 widen8(int lo, int hi)
 {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
@@ -109,127 +109,183 @@ __device__ __forceinline__ i32x4 widen(int lo, int hi)
                  __builtin_bit_cast(int, c), __builtin_bit_cast(int, d)};
 }
 
-// acc[q][i] += W_q[16 rows] X^T over channels [k0, k1) for MT groups of 16
-// tokens. wp[q]: the lane's weight row; xp[i]: the lane's token row (null:
-// none, zeros); ws[q]: the weight rows' block scales over channels.
-template <bool FP8, int G, int MT>
-__device__ __forceinline__ void stream_products(const char *const (&wp)[G],
-                                                const float *const (&ws)[G],
-                                                const uint16_t *const (&xp)[MT], int k0, int k1,
-                                                f32x4 (&acc)[G][MT])
+// No nontemporal hint: a fragment's rows are read in two halves of a 128-byte
+// line, and with the hint the second half came from memory again (up launch
+// at 48 tokens 837 us against 696).
+__device__ __forceinline__ i32x4 load_weights(const char *p)
 {
-    const int g4 = lane_id() >> 4;
-    const i32x4 zero{0, 0, 0, 0};
-    if constexpr (FP8) {
-        for (int k = k0; k < k1; k += 128) {
-            i32x4 wv[G][2];
+    return *reinterpret_cast<const i32x4 *>(p);
+}
+
+// What a wave needs for 128 bytes of every weight row: G fragments of 16
+// weight rows and MT of 16 tokens.
+template <bool FP8, int G, int MT>
+struct Step {
+    static constexpr int kX = FP8 ? 4 : 2;  // 16-byte pieces of a token per lane
+    i32x4 w[G][2], x[MT][kX];
+    float s[G];
+    // wp, xp: the lane's rows; s: the step
+    __device__ __forceinline__ void load(const char *const (&wp)[G], const float *const (&ws)[G],
+                                         const char *const (&xp)[MT], int s_)
+    {
+        const int g4 = lane_id() >> 4;
+#pragma unroll
+        for (int q = 0; q < G; ++q) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                w[q][u] = load_weights(wp[q] + (size_t)s_ * 128 + u * 64 + g4 * 16);
+            if (FP8)
+                s[q] = ws[q][s_];
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int v = 0; v < kX; ++v)
+                x[i][v] = *reinterpret_cast<const i32x4 *>(
+                    xp[i] + (FP8 ? (size_t)s_ * 256 + (v >> 1) * 128 + g4 * 32 + (v & 1) * 16
+                                 : (size_t)s_ * 128 + v * 64 + g4 * 16));
+    }
+    // the last, partial step of bf16 rows: zeros past their end
+    __device__ __forceinline__ void load_tail(const char *const (&wp)[G],
+                                              const char *const (&xp)[MT], int s_, int bytes)
+    {
+        const int g4 = lane_id() >> 4;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int at = u * 64 + g4 * 16;
+            const bool in = at < bytes;
 #pragma unroll
             for (int q = 0; q < G; ++q)
+                w[q][u] = in ? load_weights(wp[q] + (size_t)s_ * 128 + at) : i32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    wv[q][u] = *reinterpret_cast<const i32x4 *>(wp[q] + k + u * 64 + g4 * 16);
+            for (int i = 0; i < MT; ++i)
+                x[i][u] = in ? *reinterpret_cast<const i32x4 *>(xp[i] + (size_t)s_ * 128 + at)
+                             : i32x4{0, 0, 0, 0};
+        }
+    }
+    __device__ __forceinline__ void multiply(f32x4 (&acc)[G][MT]) const
+    {
+        if constexpr (FP8) {
             f32x4 p[G][MT];
 #pragma unroll
             for (int q = 0; q < G; ++q)
+#pragma unroll
                 for (int i = 0; i < MT; ++i)
                     p[q][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                i32x4 xv[MT][2];
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        xv[i][b] = xp[i] ? *reinterpret_cast<const i32x4 *>(xp[i] + k + u * 64 +
-                                                                            g4 * 16 + b * 8)
-                                         : zero;
+            for (int v = 0; v < 4; ++v)
 #pragma unroll
                 for (int q = 0; q < G; ++q) {
-                    const i32x4 w0 = widen(wv[q][u].x, wv[q][u].y);
-                    const i32x4 w1 = widen(wv[q][u].z, wv[q][u].w);
+                    const i32x4 r = w[q][v >> 1];
+                    const i32x4 wv = v & 1 ? widen8(r.z, r.w) : widen8(r.x, r.y);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        p[q][i] = mfma_bf16(w0, xv[i][0], p[q][i]);
-                        p[q][i] = mfma_bf16(w1, xv[i][1], p[q][i]);
-                    }
+                    for (int i = 0; i < MT; ++i)
+                        p[q][i] = mfma_bf16(wv, x[i][v], p[q][i]);
                 }
-            }
 #pragma unroll
-            for (int q = 0; q < G; ++q) {
-                const float s = ws[q][k >> 7];
+            for (int q = 0; q < G; ++q)
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        acc[q][i][c] = __builtin_fmaf(s, p[q][i][c], acc[q][i][c]);
-            }
-        }
-    } else {
-        for (int k = k0; k < k1; k += 32) {
-            const int kk = k + g4 * 8;
-            const bool in = kk < k1;
-            i32x4 wv[G];
+                        acc[q][i][c] = __builtin_fmaf(s[q], p[q][i][c], acc[q][i][c]);
+        } else {
 #pragma unroll
-            for (int q = 0; q < G; ++q)
-                wv[q] = in ? *reinterpret_cast<const i32x4 *>(wp[q] + 2 * (size_t)kk) : zero;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const i32x4 xv =
-                    in && xp[i] ? *reinterpret_cast<const i32x4 *>(xp[i] + kk) : zero;
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int q = 0; q < G; ++q)
-                    acc[q][i] = mfma_bf16(wv[q], xv, acc[q][i]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        acc[q][i] = mfma_bf16(w[q][u], x[i][u], acc[q][i]);
+        }
+    }
+};
+
+// acc[q][i] = W_q X_i^T over the steps [s0, s1) of rows of `bytes` bytes, the
+// loads of D steps under way at a time.
+template <bool FP8, int G, int MT, int D>
+__device__ __forceinline__ void stream_products(const char *const (&wp)[G],
+                                                const float *const (&ws)[G],
+                                                const char *const (&xp)[MT], int s0, int s1,
+                                                int64_t bytes, f32x4 (&acc)[G][MT])
+{
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            acc[q][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int full = min(s1, (int)(bytes >> 7));
+    if (s0 < full) {
+        Step<FP8, G, MT> buf[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            buf[d].load(wp, ws, xp, min(s0 + d, full - 1));
+        for (int s = s0; s < full; s += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (s + d < full)
+                    buf[d].multiply(acc);
+                buf[d].load(wp, ws, xp, min(s + d + D, full - 1));
             }
         }
+    }
+    if (!FP8 && full < s1) {
+        Step<FP8, G, MT> t;
+        t.load_tail(wp, xp, full, (int)(bytes & 127));
+        t.multiply(acc);
     }
 }
 
 // First launch: 16 columns of f, gate and up, for every token of one expert.
-// The block's waves split the channels of h.
-template <bool FP8, int MT>
-__device__ void up_tile(const DecodeArgs &a, const Groups &g, int e, int n0,
-                        float (&part)[kWaves][2][64][17])
+// The block's waves split the channels of h; their sums meet in LDS, part
+// [wave][gate, up][token][17].
+template <bool FP8, int MT, int D>
+__device__ __forceinline__ void up_tile(const DecodeArgs &a, const Groups &g, int e, int n0,
+                                        int m0, float *part)
 {
+    constexpr int kThreads = kUpWaves * kWave;
     const int tid = threadIdx.x, lane = lane_id(), wave = tid >> 6, l16 = lane & 15;
-    const int first = g.start[e], rows = g.start[e + 1] - first;
-    const size_t esize = FP8 ? 1 : 2;
-    const int step = FP8 ? 128 : 32;
-    const int units = (a.h + step - 1) / step;
-    const int k0 = units * wave / kWaves * step, k1 = min(units * (wave + 1) / kWaves * step, a.h);
+    const int first = g.start[e] + m0, rows = min(g.start[e + 1] - first, 16 * MT);
+    const int64_t bytes = (int64_t)a.h * (FP8 ? 1 : 2);
+    const int steps = (int)((bytes + 127) >> 7);
+    const int s0 = steps * wave / kUpWaves, s1 = steps * (wave + 1) / kUpWaves;
     const int n = min(n0 + l16, a.f - 1);
     const char *wp[2];
     const float *ws[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         wp[q] = static_cast<const char *>(a.w13) +
-                ((size_t)e * 2 * a.f + (size_t)q * a.f + n) * a.h * esize;
-        ws[q] = FP8 ? a.s13 + ((size_t)e * (2 * a.f >> 7) + ((q * a.f + n0) >> 7)) * (a.h >> 7)
+                ((int64_t)e * 2 * a.f + (int64_t)q * a.f + n) * bytes;
+        ws[q] = FP8 ? a.s13 + ((int64_t)e * (2 * a.f >> 7) + ((q * a.f + n0) >> 7)) * (a.h >> 7)
                     : nullptr;
     }
-    const uint16_t *xp[MT];
+    // a fragment's rows past the expert's last repeat it: their results are
+    // columns of their own, not used
+    const char *xp[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = i * 16 + l16;
-        xp[i] = m < rows ? a.x + (size_t)(g.entry[first + m] / a.K) * a.h : nullptr;
-    }
+    for (int i = 0; i < MT; ++i)
+        xp[i] = reinterpret_cast<const char *>(
+            a.x + (size_t)(g.entry[first + min(i * 16 + l16, rows - 1)] / a.K) * a.h);
     f32x4 acc[2][MT];
+    stream_products<FP8, 2, MT, D>(wp, ws, xp, s0, s1, bytes, acc);
+    const int T = a.T;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-        for (int i = 0; i < MT; ++i)
-            acc[q][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    stream_products<FP8, 2, MT>(wp, ws, xp, k0, k1, acc);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
         for (int i = 0; i < MT; ++i)
-            for (int c = 0; c < 4; ++c)
-                part[wave][q][i * 16 + l16][(lane >> 4) * 4 + c] = acc[q][i][c];
+            if (i * 16 + l16 < rows)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    part[((wave * 2 + q) * T + i * 16 + l16) * 17 + (lane >> 4) * 4 + c] =
+                        acc[q][i][c];
     __syncthreads();
     for (int v = tid; v < rows * 16; v += kThreads) {
         const int m = v >> 4, c = v & 15;
         float gate = 0.0f, up = 0.0f;
-        for (int w = 0; w < kWaves; ++w) {
-            gate += part[w][0][m][c];
-            up += part[w][1][m][c];
+#pragma unroll
+        for (int w = 0; w < kUpWaves; ++w) {
+            gate += part[((w * 2) * T + m) * 17 + c];
+            up += part[((w * 2 + 1) * T + m) * 17 + c];
         }
         if (n0 + c < a.f)
             a.act[(size_t)g.entry[first + m] * a.f + n0 + c] =
@@ -239,96 +295,111 @@ __device__ void up_tile(const DecodeArgs &a, const Groups &g, int e, int n0,
 }
 
 template <bool FP8>
-__global__ __launch_bounds__(kThreads) void decode_up_kernel(DecodeArgs a)
+__global__ __launch_bounds__(kUpWaves *kWave, 4) void decode_up_kernel(DecodeArgs a)
 {
     __shared__ Groups g;
-    __shared__ float part[kWaves][2][64][17];
-    group_entries(a, g);
+    extern __shared__ float part[];
+    group_entries<kUpWaves>(a, g);
     const int nt = (a.f + 15) / 16;
     const int total = g.n_active * nt;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const int e = g.active[t / nt], n0 = t % nt * 16;
-        const int rows = g.start[e + 1] - g.start[e];
-        if (rows <= 16)
-            up_tile<FP8, 1>(a, g, e, n0, part);
-        else
-            up_tile<FP8, 4>(a, g, e, n0, part);
+        const int e = __builtin_amdgcn_readfirstlane(g.active[t / nt]), n0 = t % nt * 16;
+        const int rows = __builtin_amdgcn_readfirstlane(g.start[e + 1] - g.start[e]);
+        for (int m0 = 0; m0 < rows; m0 += 32)
+            if (rows - m0 <= 16)
+                up_tile<FP8, 1, 1>(a, g, e, n0, m0, part);
+            else
+                up_tile<FP8, 2, 1>(a, g, e, n0, m0, part);
     }
 }
 
 // Second launch: 16 columns of h for all tokens. The block's waves take the
-// active experts in turn, each with sums of its own, which are added in wave
-// order at the end: the result does not depend on timing.
-template <bool FP8, int MT>
-__device__ void down_tile(const DecodeArgs &a, const Groups &g, int e, int n0,
-                          float (&sum)[kDecodeMaxTokens][16])
+// active experts in turn (few experts: shares of their channels), each with
+// sums of its own [wave][token][16], which are added in wave order at the
+// end: the result does not depend on timing.
+template <bool FP8, int MT, int D>
+__device__ __forceinline__ void down_tile(const DecodeArgs &a, const Groups &g, int e, int n0,
+                                          int m0, int s0, int s1, float *sum)
 {
     const int lane = lane_id(), l16 = lane & 15, g4 = lane >> 4;
-    const int first = g.start[e], rows = g.start[e + 1] - first;
+    const int first = g.start[e] + m0, rows = min(g.start[e + 1] - first, 16 * MT);
+    const int64_t bytes = (int64_t)a.f * (FP8 ? 1 : 2);
     const int n = min(n0 + l16, a.h - 1);
-    const char *wp[1] = {static_cast<const char *>(a.w2) +
-                         ((size_t)e * a.h + n) * a.f * (FP8 ? 1 : 2)};
+    const char *wp[1] = {static_cast<const char *>(a.w2) + ((int64_t)e * a.h + n) * bytes};
     const float *ws[1] = {
-        FP8 ? a.s2 + ((size_t)e * ((a.h + 127) >> 7) + (n0 >> 7)) * (a.f >> 7) : nullptr};
-    const uint16_t *xp[MT];
-    int token[MT];
-    float weight[MT];
+        FP8 ? a.s2 + ((int64_t)e * ((a.h + 127) >> 7) + (n0 >> 7)) * (a.f >> 7) : nullptr};
+    const char *xp[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int m = i * 16 + l16;
-        xp[i] = nullptr;
-        token[i] = -1;
-        weight[i] = 0.0f;
-        if (m < rows) {
-            const int j = g.entry[first + m];
-            token[i] = j / a.K;
-            xp[i] = a.act + (size_t)j * a.f;
-            for (int k = j; k < (token[i] + 1) * a.K; ++k)  // repeats of the expert included
-                if (a.idx[k] == e)
-                    weight[i] += a.topw[k];
-        }
-    }
+    for (int i = 0; i < MT; ++i)
+        xp[i] = reinterpret_cast<const char *>(
+            a.act + (size_t)g.entry[first + min(i * 16 + l16, rows - 1)] * a.f);
     f32x4 acc[1][MT];
+    stream_products<FP8, 1, MT, D>(wp, ws, xp, s0, s1, bytes, acc);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        acc[0][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    stream_products<FP8, 1, MT>(wp, ws, xp, 0, a.f, acc);
+        if (i * 16 + l16 < rows) {
+            const int j = g.entry[first + i * 16 + l16], t = j / a.K;
+            float weight = 0.0f;
+            for (int k = j; k < (t + 1) * a.K; ++k)  // repeats of the expert included
+                if (a.idx[k] == e)
+                    weight += a.topw[k];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-        if (token[i] >= 0)
             for (int c = 0; c < 4; ++c) {
-                float &s = sum[token[i]][g4 * 4 + c];
-                s = __builtin_fmaf(weight[i], acc[0][i][c], s);
+                float &s = sum[t * 16 + g4 * 4 + c];
+                s = __builtin_fmaf(weight, acc[0][i][c], s);
             }
+        }
 }
 
 template <bool FP8>
-__global__ __launch_bounds__(kThreads) void decode_down_kernel(DecodeArgs a)
+__global__ __launch_bounds__(kDownWaves *kWave, 4) void decode_down_kernel(DecodeArgs a)
 {
+    constexpr int kThreads = kDownWaves * kWave;
     __shared__ Groups g;
-    __shared__ float sum[kWaves][kDecodeMaxTokens][16];
-    const int tid = threadIdx.x, wave = tid >> 6;
-    group_entries(a, g);
-    for (int v = tid; v < kWaves * kDecodeMaxTokens * 16; v += kThreads)
-        (&sum[0][0][0])[v] = 0.0f;
-    __syncthreads();
+    extern __shared__ float sum[];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    for (int v = tid; v < kDownWaves * a.T * 16; v += kThreads)
+        sum[v] = 0.0f;
+    group_entries<kDownWaves>(a, g);
     const int n0 = blockIdx.x * 16;
-    for (int i = wave; i < g.n_active; i += kWaves) {
-        const int e = g.active[i];
-        if (g.start[e + 1] - g.start[e] <= 16)
-            down_tile<FP8, 1>(a, g, e, n0, sum[wave]);
-        else
-            down_tile<FP8, 4>(a, g, e, n0, sum[wave]);
+    const int steps = (int)(((int64_t)a.f * (FP8 ? 1 : 2) + 127) >> 7);
+    const int n_active = __builtin_amdgcn_readfirstlane(g.n_active);
+    // parts of the channels, so that there is one for every wave
+    const int parts = n_active >= kDownWaves ? 1
+                                             : min((kDownWaves + n_active - 1) / max(n_active, 1),
+                                                   steps);
+    for (int i = wave; i < n_active * parts; i += kDownWaves) {
+        const int e = __builtin_amdgcn_readfirstlane(g.active[i / parts]), p = i % parts;
+        const int s0 = steps * p / parts, s1 = steps * (p + 1) / parts;
+        const int rows = __builtin_amdgcn_readfirstlane(g.start[e + 1] - g.start[e]);
+        float *const own = sum + wave * a.T * 16;
+        for (int m0 = 0; m0 < rows; m0 += 32)
+            if (rows - m0 <= 16)
+                down_tile<FP8, 1, FP8 ? 1 : 4>(a, g, e, n0, m0, s0, s1, own);
+            else
+                down_tile<FP8, 2, FP8 ? 1 : 2>(a, g, e, n0, m0, s0, s1, own);
     }
     __syncthreads();
     for (int v = tid; v < a.T * 16; v += kThreads) {
         const int t = v >> 4, c = v & 15;
         float s = 0.0f;
-        for (int w = 0; w < kWaves; ++w)
-            s += sum[w][t][c];
+#pragma unroll
+        for (int w = 0; w < kDownWaves; ++w)
+            s += sum[w * a.T * 16 + v];
         if (n0 + c < a.h)
             a.out[(size_t)t * a.h + n0 + c] = (uint16_t)f32_to_bf16(s);
     }
+}
+
+template <bool FP8>
+void launch(const DecodeArgs &a, hipStream_t stream)
+{
+    const int64_t items = (int64_t)(a.E < a.T * a.K ? a.E : a.T * a.K) * ((a.f + 15) / 16);
+    const int64_t up = items < 4ll * a.cus ? items : 4ll * a.cus;
+    hipLaunchKernelGGL(decode_up_kernel<FP8>, dim3((unsigned)up), dim3(kUpWaves * kWave),
+                       kUpWaves * 2 * a.T * 17 * sizeof(float), stream, a);
+    hipLaunchKernelGGL(decode_down_kernel<FP8>, dim3((unsigned)((a.h + 15) / 16)),
+                       dim3(kDownWaves * kWave), kDownWaves * a.T * 16 * sizeof(float), stream, a);
 }
 
 }  // namespace
@@ -337,16 +408,10 @@ hipError_t launch_moe_decode(const DecodeArgs &a, bool fp8, hipStream_t stream)
 {
     if (a.T == 0)
         return hipSuccess;
-    const int64_t items = (int64_t)(a.E < a.T * a.K ? a.E : a.T * a.K) * ((a.f + 15) / 16);
-    const unsigned up = (unsigned)(items < 4ll * a.cus ? items : 4ll * a.cus);
-    const unsigned down = (unsigned)((a.h + 15) / 16);
-    if (fp8) {
-        hipLaunchKernelGGL(decode_up_kernel<true>, dim3(up), dim3(kThreads), 0, stream, a);
-        hipLaunchKernelGGL(decode_down_kernel<true>, dim3(down), dim3(kThreads), 0, stream, a);
-    } else {
-        hipLaunchKernelGGL(decode_up_kernel<false>, dim3(up), dim3(kThreads), 0, stream, a);
-        hipLaunchKernelGGL(decode_down_kernel<false>, dim3(down), dim3(kThreads), 0, stream, a);
-    }
+    if (fp8)
+        launch<true>(a, stream);
+    else
+        launch<false>(a, stream);
     return hipGetLastError();
 }
 
