@@ -14,7 +14,7 @@ EPX_OK, EPX_EINVAL, EPX_ECAPACITY, EPX_EUNSUPPORTED, EPX_EHIP, EPX_EDEVICE = 0, 
 DEV_BAD_ROUTE, DEV_OVERFLOW, DEV_BAD_HANDLE, DEV_WORKSPACE = 1, 2, 4, 8
 MAX_TOPK, MAX_EXPERTS, MAX_RANKS, MAX_SWEEP_GBPS = 32, 512, 64, 100000
 NOALLOC_SCRATCH_BYTES = 1 << 20
-MAX_CHANNELS, MAX_DECODE_TOKENS = 65536, 64
+MAX_CHANNELS, MAX_DECODE_TOKENS, MAX_EXPERT_BYTES = 65536, 64, 0xFFFF0000
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int

@@ -685,6 +685,10 @@ static int grouped_args(epx_ctx *ctx, const void *x, const float *x_scales, int6
     if (n_rows < 0 || n_rows > INT32_MAX || L < 1 || L > EPX_MAX_EXPERTS ||
         K > EPX_MAX_CHANNELS || N > EPX_MAX_CHANNELS)
         return EPX_EINVAL;
+    // the kernels address one expert's weights with 32 bits
+    const int64_t kbytes = fp8 ? (int64_t)K : 2 * (int64_t)K;
+    if ((gated ? 2 : 1) * (int64_t)N * kbytes > EPX_MAX_EXPERT_BYTES)
+        return EPX_EINVAL;
     if ((rc = check_hidden(K, fp8)) != EPX_OK || (rc = check_hidden(N, gated && fp8)) != EPX_OK)
         return rc;
     if (n_rows > 0) {
@@ -730,6 +734,10 @@ static int ll_grouped(epx_ctx *ctx, const void *x, const float *x_scales, int K,
                                 fp8, gated, out, out_scales, a);
     if (rc != EPX_OK)
         return rc;
+    // ... and, over several sources, one expert's regions
+    if (R_buf > 1 && (int64_t)R_buf * cap * (fp8 ? (int64_t)K + 4 * epx::scale_stride(K)
+                                                 : 2 * (int64_t)K) > EPX_MAX_EXPERT_BYTES)
+        return EPX_EINVAL;
     a.counts = ll_count; a.R_buf = R_buf; a.cap = cap;
     return launched(epx::launch_grouped(a, fp8 != 0, gated, stream));
 }

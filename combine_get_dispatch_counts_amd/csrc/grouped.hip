@@ -42,7 +42,9 @@ struct Shape {
     static constexpr bool kFp8Rows = MODE != kBf16;
     static constexpr int kEsize = kFp8Rows ? 1 : 2;
     static constexpr int kMF = BM / 16 / kWM;      // row fragments of a wave
-    static constexpr int kALoads = BM / 8 / kWaves;  // 8-row loads of a wave and step
+    // 8-row loads of a wave and step (the last one not of every wave, if BM
+    // is no multiple of 64)
+    static constexpr int kALoads = (BM + 63) / 64;
     static constexpr int kWLoads = kBN / 8 / kWaves;
     static constexpr int kLoads = kALoads + kWLoads;
     static constexpr int kXStep = BM * kRow, kWStep = kBN * kRow;  // bytes of a step
@@ -50,8 +52,9 @@ struct Shape {
     // issued after its own, are under way (an iteration issues rows, then weights).
     static constexpr int XA = XBUF - 1, WA = WBUF - 1;
     static_assert(WA >= XA && XA >= 1, "");
-    static constexpr int kUnderWay = (XA - 1) * kLoads + (WA > XA ? kWLoads : 0);
-    static constexpr int kScale = kFp8Rows ? (BM + kWave) * 16 : 0;  // 4 steps of scales
+    static constexpr int kUnderWay = (XA - 1) * (BM / 64 + kWLoads) + (WA > XA ? kWLoads : 0);
+    static constexpr int kScaleRows = (BM + kWave - 1) / kWave * kWave;
+    static constexpr int kScale = kFp8Rows ? (kScaleRows + kWave) * 16 : 0;  // 4 steps of scales
     static constexpr int kAmax = GATED && kFp8Rows ? kWN * BM * 4 : 0;
     static constexpr int kTiles = 2064;            // running row tiles of the experts
     static constexpr int kRing = WBUF + 1;         // tiles opened and not yet finished
@@ -166,7 +169,7 @@ template <Mode MODE, bool GATED, int BM, int XBUF, int WBUF>
 __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 {
     using S = Shape<MODE, GATED, BM, XBUF, WBUF>;
-    constexpr int MF = S::kMF;
+    constexpr int MF = S::kMF, kScaleWaves = (BM + kWave - 1) / kWave;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     float *const row_amax = reinterpret_cast<float *>(smem + S::kAmaxAt);
     int *const tiles_before = reinterpret_cast<int *>(smem + S::kTilesAt);
@@ -339,7 +342,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                 }
                 if constexpr (S::kFp8Rows) {
                     const int st = scale_stride(a.K);
-                    if (wave < BM / kWave) {
+                    if (wave < kScaleWaves) {
                         sr = buffer_of(a.xs + base * st, (a.n_rows - base) * st * 4);
                         const int m = min(wave * kWave + lane, o.rows - 1);
                         const int row = gather ? expert_row(a, o.e, o.m0 + m) : m;
@@ -362,7 +365,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         }
         if constexpr (S::kFp8Rows) {
             if ((xstep & 3) == 0) {
-                if (wave <= BM / kWave)
+                if (wave <= kScaleWaves)
                     load_lds(uniform(lds0 + S::kScaleAt + xgroup * S::kScale + wave * 1024), sr,
                              soff, (uint32_t)xstep * 4);
                 xgroup = xgroup + 1 == XBUF ? 0 : xgroup + 1;
@@ -375,6 +378,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         }
     };
     const auto load_rows = [&](int i) {
+        if (BM % 64 && (i * kWaves + wave) * 8 >= BM)
+            return;
         load_lds(uniform(lds0 + xbuf * S::kXStep + (i * kWaves + wave) * 1024), xr, xoff[i],
                  (uint32_t)xstep * kRow);
     };
@@ -435,19 +440,29 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                                         pos));
         float sw[2] = {0.0f, 0.0f};
         if constexpr (S::kFp8Rows) {
-            sw[0] = *reinterpret_cast<const float *>(sc + (BM + (GATED ? 0 : wn >> 1)) * 16);
+            sw[0] = *reinterpret_cast<const float *>(sc + (S::kScaleRows + (GATED ? 0 : wn >> 1)) * 16);
             if (GATED)
-                sw[1] = *reinterpret_cast<const float *>(sc + (BM + 1) * 16);
+                sw[1] = *reinterpret_cast<const float *>(sc + (S::kScaleRows + 1) * 16);
         }
         begin_weights();
         begin_rows();
-        // The wave's row fragments two at a time, as far as the tile has rows;
-        // the next step's loads go between the first products. Fragment i + 1
-        // is read while the matrix unit works on fragment i; FP8 sums are
-        // scaled and added kLag products after their own.
-        const auto part = [&](auto from, auto count, auto loads) {
+        // The wave's row fragments two at a time, as far as the tile has rows.
+        // Fragment i + 1 is read while the matrix unit works on fragment i.
+        // The step's loads go between the products: where there is time for
+        // them to arrive, evenly, as a wave that issues them faster than 64
+        // bytes a cycle and compute unit waits; with two buffers, early.
+        constexpr int kOver = XBUF >= 3 || MODE == kWide ? MF : 2;  // fragments
+        const auto piece_at = [&](int i) {
+            return (i < kOver ? i : kOver) * S::kLoads / kOver;
+        };
+        const auto load_piece = [&](int p) {
+            if (p < S::kALoads)
+                load_rows(p);
+            else
+                load_weights(p - S::kALoads);
+        };
+        const auto part = [&](auto from, auto count) {
             constexpr int I0 = decltype(from)::value, I1 = I0 + decltype(count)::value;
-            constexpr int kPer = (decltype(loads)::value + I1 - I0 - 1) / (I1 - I0);
             float sx[I1 - I0];
             if constexpr (S::kFp8Rows) {
 #pragma unroll
@@ -455,21 +470,18 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                     sx[i - I0] =
                         *reinterpret_cast<const float *>(sc + ((i * kWM + wm) * 16 + l16) * 16);
             }
-            // FP8 results on their way: kPair of the four weight fragments at
-            // a time (widened codes: two chains of four products, so that no
-            // product waits for the one before it)
-            constexpr int kPair = MODE == kWide ? 2 : 1, kLag = MODE == kWide ? 2 : 3;
-            f32x4 d[kLag + kPair];
-            const auto add = [&](int q) {
-                const int i = q >> 2, j = q & 3;
-                const float sc_ = sx[i] * sw[GATED && j >= 2];
+            // an FP8 fragment's products are scaled and added between the
+            // products of the next one
+            f32x4 d[2][4];
+            const auto add = [&](int i, int j) {
+                const float sc_ = sx[i - I0] * sw[GATED && j >= 2];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float v = __builtin_fmaf(sc_, d[q % (kLag + kPair)][c], acc[j][I0 + i][c]);
+                    float v = __builtin_fmaf(sc_, d[i & 1][j][c], acc[j][i][c]);
                     // keeps the sum here: moved behind a branch between the
                     // parts, it would hold its operands until then
                     asm volatile("" : "+v"(v));
-                    acc[j][I0 + i][c] = v;
+                    acc[j][i][c] = v;
                 }
             };
 #pragma unroll
@@ -477,25 +489,27 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                 const Frag<MODE> xf(x);
                 if (i + 1 < MF)
                     x = Raw::read(xb + (i + 1) * kWM * 16 * kRow, pos);
-                if constexpr (S::kFp8Rows) {
+                if constexpr (MODE == kFp8) {
 #pragma unroll
-                    for (int j = 0; j < 4; j += kPair) {
-                        const int q = (i - I0) * 4 + j;
-                        f32x4 t[kPair];
+                    for (int j = 0; j < 4; ++j) {
+                        d[i & 1][j] = multiply<MODE>(w[j], xf, 0, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                        if (i > I0)
+                            add(i - 1, j);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                } else if constexpr (MODE == kWide) {
+                    // four chains of four products, so that no product waits
+                    // for the one before it
 #pragma unroll
-                        for (int u = 0; u < kPair; ++u)
-                            t[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int j = 0; j < 4; ++j)
+                        d[i & 1][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int k = 0; k < Frag<MODE>::kProducts; ++k)
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                            for (int u = 0; u < kPair; ++u)
-                                t[u] = multiply<MODE>(w[j + u], xf, k, t[u]);
-#pragma unroll
-                        for (int u = 0; u < kPair; ++u) {
-                            d[(q + u) % (kLag + kPair)] = t[u];
-                            if (q + u >= kLag)
-                                add(q + u - kLag);
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            d[i & 1][j] = multiply<MODE>(w[j], xf, k, d[i & 1][j]);
+                        if (i > I0)
+                            add(i - 1, k);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 } else {
@@ -506,33 +520,40 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                             acc[j][i] = multiply<MODE>(w[j], xf, k, acc[j][i]);
                 }
 #pragma unroll
-                for (int p = (i - I0) * kPer; p < (i - I0 + 1) * kPer; ++p)
-                    if (p < decltype(loads)::value) {
-                        if (p < S::kALoads)
-                            load_rows(p);
-                        else
-                            load_weights(p - S::kALoads);
-                    }
+                for (int p = piece_at(i); p < piece_at(i + 1); ++p)
+                    load_piece(p);
                 __builtin_amdgcn_sched_barrier(0);
             }
             if constexpr (S::kFp8Rows) {
 #pragma unroll
-                for (int q = (I1 - I0) * 4 - kLag; q < (I1 - I0) * 4; ++q)
-                    add(q);
+                for (int j = 0; j < 4; ++j)
+                    add(I1 - 1, j);
             }
         };
-        part(Const<0>{}, Const<2>{}, Const<S::kLoads>{});
+        // the loads of the parts left out
+        const auto rest = [&](int i0) {
+#pragma unroll
+            for (int p = 0; p < S::kLoads; ++p)
+                if (p >= piece_at(i0))
+                    load_piece(p);
+        };
+        part(Const<0>{}, Const<2>{});
+        if (MF > 2 && mf > 2) {
+            part(Const<(MF > 2 ? 2 : 0)>{}, Const<2>{});
+            if (MF > 4 && mf > 4) {
+                part(Const<(MF > 4 ? 4 : 0)>{}, Const<(MF > 5 ? 2 : 1)>{});
+                if (MF > 6 && mf > 6)
+                    part(Const<(MF > 6 ? 6 : 0)>{}, Const<2>{});
+                else if (MF > 6)
+                    rest(6);
+            } else if (MF > 4) {
+                rest(4);
+            }
+        } else if (MF > 2) {
+            rest(2);
+        }
         end_rows();
         end_weights();
-        if constexpr (MF > 2)
-            if (mf > 2)
-                part(Const<2>{}, Const<2>{}, Const<0>{});
-        if constexpr (MF > 4)
-            if (mf > 4)
-                part(Const<4>{}, Const<2>{}, Const<0>{});
-        if constexpr (MF > 6)
-            if (mf > 6)
-                part(Const<6>{}, Const<2>{}, Const<0>{});
         xcur = xcur + 1 == XBUF ? 0 : xcur + 1;
         wcur = wcur + 1 == WBUF ? 0 : wcur + 1;
         if ((s & 3) == 3 || s + 1 == steps)
@@ -658,22 +679,25 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
 // Tile height and buffers by the rows an expert has on average (regions: by
 // the rows they hold), which is all the host knows. Few rows: the weights'
 // stream decides, and three steps of both operands in LDS keep more of it
-// under way (128 regions of 4 rows, FP8 gated: 1300 us, against 1510 for 192
+// under way (256 regions of 4 rows, FP8 gated: 1270 us, against 1510 for 160
 // rows with two steps of rows and three of weights). Around 128 rows: one
-// tile per expert (gated FP8, 256 experts of 128 rows: 2310 us, against 2950
-// for 128-row tiles). Many: the fewest bytes per product (bf16, 3700 rows:
-// 774 us against 804; FP8, 770 rows: 500 against 514).
+// tile per expert (gated FP8, 256 experts of 128 rows: 2230 us, against 2960
+// for 128-row tiles; bf16 has room for three steps of 160 rows: 336 us for 94
+// rows on average, against 371). Many: the fewest bytes per product (bf16,
+// 3700 rows: 780 us against 830; FP8, 770 rows: 500 against 540).
 template <Mode MODE, bool GATED>
 hipError_t pick(const GroupedArgs &a, hipStream_t stream)
 {
     const int64_t per = a.n_rows / a.L;
-    if (per <= (a.off ? 96 : 128))
-        return launch<MODE, GATED, 128, 3, 3>(a, stream);
     if constexpr (MODE != kWide) {
         if (a.off && per > 384)
             return launch<MODE, GATED, 256, 2, 2>(a, stream);
     }
-    return launch<MODE, GATED, 192, 2, 3>(a, stream);
+    if constexpr (MODE == kBf16)
+        return launch<MODE, GATED, 160, 3, 3>(a, stream);
+    else
+        return per <= (a.off ? 96 : 128) ? launch<MODE, GATED, 128, 3, 3>(a, stream)
+                                         : launch<MODE, GATED, 160, 2, 3>(a, stream);
 }
 
 }  // namespace

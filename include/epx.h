@@ -69,6 +69,7 @@ extern "C" {
 #define EPX_MAX_SWEEP_GBPS 100000
 #define EPX_MAX_CHANNELS 65536      /* K, N and f of the experts' products */
 #define EPX_MAX_DECODE_TOKENS 64    /* T of epx_moe_decode */
+#define EPX_MAX_EXPERT_BYTES 0xFFFF0000ll /* one expert's matrix (w13: both halves) */
 #define EPX_NOALLOC_SCRATCH_BYTES (1u << 20) /* see epx_get_dispatch_layout_noalloc */
 
 typedef struct epx_ctx epx_ctx;
@@ -462,7 +463,8 @@ int epx_quantize_weights(epx_ctx *ctx, const uint16_t *w, int E, int N, int K, u
  *      expert are left as they were. The same inputs give the same bytes.
  * Offsets that decrease or leave [0, n_rows] set EPX_DEV_OVERFLOW and are
  * clamped. 1 <= L <= 512, 0 <= n_rows <= 2^31 - 1, K and N at most
- * EPX_MAX_CHANNELS. Buffers 16-byte aligned; out must not overlap an input. */
+ * EPX_MAX_CHANNELS, one expert's w at most EPX_MAX_EXPERT_BYTES. Buffers
+ * 16-byte aligned; out must not overlap an input. */
 int epx_grouped_gemm(epx_ctx *ctx, const void *x, const float *x_scales, int64_t n_rows, int K,
                      const void *w, const float *w_scales, int L, int N, int fp8,
                      const int32_t *off, uint16_t *out, hipStream_t stream);
@@ -487,7 +489,8 @@ int epx_grouped_swiglu(epx_ctx *ctx, const void *x, const float *x_scales, int64
  * layout; the counts are read on the device, and a negative count -- nothing
  * arrived -- is none). Rows past a region's count are neither read nor
  * written. A count above cap sets EPX_DEV_OVERFLOW and is clamped. L * R_buf
- * * cap must fit in int32, R_buf <= 64. */
+ * * cap must fit in int32, R_buf <= 64; with R_buf > 1 one expert's R_buf * cap
+ * rows (FP8: codes and scales) at most EPX_MAX_EXPERT_BYTES. */
 int epx_ll_grouped_gemm(epx_ctx *ctx, const void *x, const float *x_scales, int K, const void *w,
                         const float *w_scales, int L, int N, int fp8, const int32_t *ll_count,
                         int R_buf, int cap, uint16_t *out, hipStream_t stream);
