@@ -32,7 +32,8 @@ def _ctx(device: torch.device) -> ctypes.c_void_p:
 
 
 def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    idx = device.index if device.index is not None else torch.cuda.current_device()
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(idx))
 
 
 def _p(t: torch.Tensor | None) -> ctypes.c_void_p | None:

@@ -47,11 +47,18 @@ __device__ __forceinline__ float silu_mul(float g, float u)
     return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
-// Rows of expert e: the first one and how many, kept inside the caller's
-// buffer (bad: the offsets or counts say otherwise).
+// Rows of a region, kept inside it (bad: the count says otherwise).
+__device__ __forceinline__ int region_rows(const GroupedArgs &a, int64_t region, bool &bad)
+{
+    const int c = a.counts[region];
+    bad |= c > a.cap;
+    return min(max(c, 0), a.cap);
+}
+
+// Rows of expert e where they lie together (expert-major, or one region):
+// the first one and how many, kept inside the caller's buffer.
 __device__ __forceinline__ int expert_rows(const GroupedArgs &a, int e, int64_t &first, bool &bad)
 {
-    bad = false;
     if (a.off) {
         const int64_t lo = a.off[e], hi = a.off[e + 1];
         int64_t b = lo < 0 ? 0 : lo, t = hi;
@@ -61,32 +68,36 @@ __device__ __forceinline__ int expert_rows(const GroupedArgs &a, int e, int64_t 
             t = a.n_rows;
         if (t < b)
             t = b;
-        bad = b != lo || t != hi;
+        bad |= b != lo || t != hi;
         first = b;
         return (int)(t - b);
     }
-    first = (int64_t)e * a.R_buf * a.cap;
-    int n = 0;
-    for (int s = 0; s < a.R_buf; ++s) {
-        const int c = a.counts[(int64_t)e * a.R_buf + s];
-        bad |= c > a.cap;
-        n += min(max(c, 0), a.cap);
-    }
-    return n;
+    first = (int64_t)e * a.cap;
+    return region_rows(a, e, bad);
 }
 
-// Row number i of expert e, counted from the expert's first row.
-__device__ __forceinline__ int expert_row(const GroupedArgs &a, int e, int i)
-{
-    if (a.off)
-        return i;
-    for (int s = 0; s < a.R_buf; ++s) {
-        const int c = min(max(a.counts[(int64_t)e * a.R_buf + s], 0), a.cap);
-        if (i < c)
-            return s * a.cap + i;
-        i -= c;
+// The rows of an expert spread over R_buf > 1 regions: lane s holds the rows
+// of the regions up to s (R_buf <= 64). Every lane of a wave takes part.
+struct Regions {
+    int upto;
+    __device__ __forceinline__ void load(const GroupedArgs &a, int e)
+    {
+        bool bad = false;
+        const int s = lane_id();
+        upto = wave_inclusive_sum(s < a.R_buf ? region_rows(a, (int64_t)e * a.R_buf + s, bad) : 0);
     }
-    return 0;  // not reached for i < expert_rows(e)
-}
+    __device__ __forceinline__ int rows() const { return __builtin_amdgcn_readlane(upto, 63); }
+    // row number i of the expert (0 <= i < rows()), counted from its first region
+    __device__ __forceinline__ int row(const GroupedArgs &a, int i) const
+    {
+        int s = 0;
+#pragma unroll
+        for (int step = 32; step; step >>= 1)
+            if (__shfl(upto, s + step - 1, kWave) <= i)
+                s += step;
+        const int before = __shfl(upto, max(s - 1, 0), kWave);
+        return s * a.cap + i - (s ? before : 0);
+    }
+};
 
 }  // namespace epx

@@ -182,15 +182,25 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 
     // row tiles of every expert, as running totals (L <= kThreads)
     static_assert(EPX_MAX_EXPERTS <= kThreads && EPX_MAX_EXPERTS * 4 + 4 <= S::kTiles, "");
+    const bool gather = !a.off && a.R_buf > 1;  // an expert's rows lie in several regions
     {
         int n = 0;
-        if (tid < a.L) {
+        bool bad = false;
+        if (gather) {
+            if (tid < a.L)
+                tiles_before[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < a.L * a.R_buf; i += kThreads)
+                atomicAdd(&tiles_before[i / a.R_buf], region_rows(a, i, bad));
+            __syncthreads();
+            n = tid < a.L ? tiles_before[tid] : 0;
+        } else if (tid < a.L) {
             int64_t first;
-            bool bad;
-            n = (expert_rows(a, tid, first, bad) + BM - 1) / BM;
-            if (bad && blockIdx.x == 0)
-                flag_error(a.err, EPX_DEV_OVERFLOW);
+            n = expert_rows(a, tid, first, bad);
         }
+        if (bad && blockIdx.x == 0)
+            flag_error(a.err, EPX_DEV_OVERFLOW);
+        n = (n + BM - 1) / BM;
         const int incl = wave_inclusive_sum(n);
         if (lane == 63)
             wave_tiles[wave] = incl;
@@ -237,9 +247,16 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         const int q = (int)(t - (int64_t)before * nt);
         const int group = q / (4 * nt), gm = min(4, mts - group * 4);
         const int r = q - group * 4 * nt;
-        int64_t first;
-        bool bad;
-        const int rows = uniform(expert_rows(a, e, first, bad));
+        int64_t first = (int64_t)e * a.R_buf * a.cap;
+        bool bad = false;
+        int rows;
+        if (gather) {
+            Regions g;
+            g.load(a, e);
+            rows = g.rows();
+        } else {
+            rows = uniform(expert_rows(a, e, first, bad));
+        }
         o.first = (int64_t)uniform64((uint64_t)first);
         o.e = e;
         o.m0 = (group * 4 + r % gm) * BM;
@@ -249,7 +266,6 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
     const int r8 = lane >> 3, c8 = lane & 7;  // a load's row and 16-byte piece
-    const bool gather = !a.off && a.R_buf > 1;
     // Behind the last tile the loads go on from empty buffers (zeros into LDS
     // that is not read again), so every step issues the same number.
 
@@ -329,13 +345,16 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
             if (o.rows > 0) {
                 // base: the first row a load may name (regions: the expert's)
                 const int64_t base = o.first + (gather ? 0 : o.m0);
+                Regions g{};
+                if (gather)
+                    g.load(a, o.e);
                 xr = buffer_of(static_cast<const char *>(a.x) + base * kbytes,
                                (a.n_rows - base) * kbytes);
 #pragma unroll
                 for (int i = 0; i < S::kALoads; ++i) {
                     const int lr = (i * kWaves + wave) * 8 + r8;  // row of the tile
                     const int m = min(lr, o.rows - 1);
-                    const int row = gather ? expert_row(a, o.e, o.m0 + m) : m;
+                    const int row = gather ? g.row(a, o.m0 + m) : m;
                     xoff[i] = (uint32_t)((int64_t)row * kbytes) + (uint32_t)((c8 ^ r8) * 16);
                     if (lr >= ((o.rows + 15) & ~15))
                         xoff[i] = kNowhere;
@@ -345,7 +364,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                     if (wave < kScaleWaves) {
                         sr = buffer_of(a.xs + base * st, (a.n_rows - base) * st * 4);
                         const int m = min(wave * kWave + lane, o.rows - 1);
-                        const int row = gather ? expert_row(a, o.e, o.m0 + m) : m;
+                        const int row = gather ? g.row(a, o.m0 + m) : m;
                         soff = (uint32_t)((int64_t)row * st * 4);
                     } else {
                         const int64_t sb = ((int64_t)o.e * nb_n + (o.n0 >> 7)) * kb_n;
@@ -563,16 +582,20 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         s = 0;
 
         // ---- epilogue: lane l holds consecutive columns of rows (2 i + wm) * 16 + l16
-        const auto out_row = [&](int m) -> int64_t {
-            return o.first + expert_row(a, o.e, o.m0 + m);
+        Regions regions{};
+        if (gather)
+            regions.load(a, o.e);
+        const auto out_row = [&](int m) -> int64_t {  // (every lane of the wave calls it)
+            return o.first + (gather ? regions.row(a, min(o.m0 + m, o.m0 + o.rows - 1)) : o.m0 + m);
         };
         if constexpr (!GATED) {
             const int n = o.n0 + wn * 64 + g4 * 16;
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
                 const int m = (i * kWM + wm) * 16 + l16;
+                const int64_t row = out_row(m);
                 if (i < mf && m < o.rows) {
-                    uint16_t *p = static_cast<uint16_t *>(a.out) + out_row(m) * a.N + n;
+                    uint16_t *p = static_cast<uint16_t *>(a.out) + row * a.N + n;
                     u32x4 v[2];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -600,6 +623,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 #pragma unroll
                 for (int i = 0; i < MF; ++i) {
                     const int m = (i * kWM + wm) * 16 + l16;
+                    const int64_t row = out_row(m);
                     if (i < mf && m < o.rows && n < a.N) {
                         u32x4 v;
 #pragma unroll
@@ -608,8 +632,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                             for (int c = 0; c < 2; ++c)
                                 v[2 * j + c] = f32_to_bf16(acc[j][i][2 * c]) |
                                                (f32_to_bf16(acc[j][i][2 * c + 1]) << 16);
-                        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) +
-                                                   out_row(m) * a.N + n) = v;
+                        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.out) + row * a.N +
+                                                   n) = v;
                     }
                 }
             } else {
@@ -632,6 +656,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 #pragma unroll
                 for (int i = 0; i < MF; ++i) {
                     const int m = (i * kWM + wm) * 16 + l16;
+                    const int64_t row = out_row(m);
                     if (i < mf && m < o.rows) {
                         float v = row_amax[m];
 #pragma unroll
@@ -644,7 +669,6 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
                                 q[j] |= e4m3_of_quotient(acc[j][i][c], s) << (8 * c);
-                        const int64_t row = out_row(m);
                         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.N + n) =
                             uint2{q[0], q[1]};
                         float *os = a.out_s + row * st;
