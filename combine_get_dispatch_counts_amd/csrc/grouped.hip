@@ -275,7 +275,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     int wstep = steps, wbuf = 0, wtile = 0;
     i32x4 wr{0, 0, 0, 0x00020000};
     uint32_t woff[S::kWLoads] = {};
-    const auto wkey = [&](int lr) { return (lr & 3) | (lr >> (GATED ? 1 : 2) & 4); };
+    const auto wkey = [&](int lr) { return (lr & 3) | (lr >> 1 & 4); };
     const auto begin_weights = [&]() {
         if (wstep == steps) {
             wstep = 0;
@@ -409,10 +409,13 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 
     // ---- products
     const int pos = (g4 ^ (l16 & 7)) * 16;  // the lane's first piece of its row, swizzled
-    // weight rows of a wave, arranged so that a lane's results over its
-    // fragments j are consecutive columns: fragment row l16 is column
-    // 16 (l16 / 4) + 4 j + l16 % 4 (gated: 8 (l16 / 4) + 4 j + l16 % 4)
-    const int wrow = GATED ? wn * 32 + (l16 >> 2) * 8 + (l16 & 3) : wn * 64 + (l16 >> 2) * 16 + (l16 & 3);
+    // weight rows of a wave, arranged so that a lane's results of fragments j
+    // and j + 1 (j even) are eight consecutive columns, and those of its row's
+    // four lanes 64 bytes or more together: fragment row l16 is column
+    // 8 (l16 / 4) + 4 (j % 2) + l16 % 4 of the fragment pair's 32 (gated: one
+    // pair gate columns, one the up rows of the same)
+    const int wrow = wn * (GATED ? 32 : 64) + (l16 >> 2) * 8 + (l16 & 3);
+    constexpr int kPairRows = GATED ? 128 : 32;
     const char *const xlane = smem + (wm * 16 + l16) * kRow;
     const char *const wlane = smem + XBUF * S::kXStep + wrow * kRow;
 
@@ -455,7 +458,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         Frag<MODE> w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            w[j] = Frag<MODE>(Raw::read(wb + (GATED ? (j >> 1) * 128 + (j & 1) * 4 : j * 4) * kRow,
+            w[j] = Frag<MODE>(Raw::read(wb + ((j >> 1) * kPairRows + (j & 1) * 4) * kRow,
                                         pos));
         float sw[2] = {0.0f, 0.0f};
         if constexpr (S::kFp8Rows) {
@@ -581,7 +584,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
             continue;
         s = 0;
 
-        // ---- epilogue: lane l holds consecutive columns of rows (2 i + wm) * 16 + l16
+        // ---- epilogue: lane l holds columns of rows (2 i + wm) * 16 + l16
         Regions regions{};
         if (gather)
             regions.load(a, o.e);
@@ -589,7 +592,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
             return o.first + (gather ? regions.row(a, min(o.m0 + m, o.m0 + o.rows - 1)) : o.m0 + m);
         };
         if constexpr (!GATED) {
-            const int n = o.n0 + wn * 64 + g4 * 16;
+            const int n = o.n0 + wn * 64 + g4 * 8;
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
                 const int m = (i * kWM + wm) * 16 + l16;
@@ -606,8 +609,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                                 (f32_to_bf16(acc[j][i][2 * c + 1]) << 16);
                     if (n < a.N)  // N is a multiple of 8
                         *reinterpret_cast<u32x4 *>(p) = v[0];
-                    if (n + 8 < a.N)
-                        *reinterpret_cast<u32x4 *>(p + 8) = v[1];
+                    if (n + 32 < a.N)
+                        *reinterpret_cast<u32x4 *>(p + 32) = v[1];
                 }
             }
         } else {
