@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     }
     constexpr int kCols = GATED ? kBN / 2 : kBN;  // output columns of a tile
     const int nt = (a.N + kCols - 1) / kCols;
-    const int64_t total = (int64_t)uniform(tiles_before[a.L]) * nt;
+    const int total = uniform(tiles_before[a.L]) * nt;  // below 2^31: checked by the launcher
     const int wrows = GATED ? 2 * a.N : a.N;
     const int kb_n = a.K >> 7, nb_n = (wrows + 127) >> 7;
     const int64_t kbytes = (int64_t)a.K * S::kEsize;
@@ -227,24 +227,24 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     // XCDs in turn: in a full round an XCD's blocks get consecutive tiles, so
     // tiles that share rows or weights share an L2.
     const int G = gridDim.x, b = blockIdx.x;
-    const auto tile_number = [&](int64_t r) -> int64_t {
-        const int64_t base = r * G;
+    const auto tile_number = [&](int r) {
+        const int base = r * G;
         if (G % 8 == 0 && total - base >= G)
             return base + (b % 8) * (G / 8) + b / 8;
         return base + b;
     };
     // Tiles of an expert: four row tiles at a time, over all columns, row
     // tiles fastest: 32 neighbours read 4 row tiles and 8 weight tiles.
-    const auto find_tile = [&](int64_t t, Tile &o) {
-        const int mt = (int)(t / nt);
-        int e = 0;
-        for (int step = 512; step; step >>= 1)
-            if (e + step < a.L && tiles_before[e + step] <= mt)
-                e += step;
+    const auto find_tile = [&](int t, Tile &o) {
+        const int mt = t / nt;
+        int e = -1;  // the last expert whose tiles begin at or before mt
+        for (int e0 = 0; e0 < a.L; e0 += kWave)
+            e += __builtin_popcountll(
+                __ballot(e0 + lane < a.L && tiles_before[min(e0 + lane, a.L)] <= mt));
         e = uniform(e);
         const int before = uniform(tiles_before[e]);
         const int mts = uniform(tiles_before[e + 1]) - before;
-        const int q = (int)(t - (int64_t)before * nt);
+        const int q = t - before * nt;
         const int group = q / (4 * nt), gm = min(4, mts - group * 4);
         const int r = q - group * 4 * nt;
         int64_t first = (int64_t)e * a.R_buf * a.cap;
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
 
     // ---- weight loads: they open the tiles
     Tile wt{};
-    int64_t wround = 0;
+    int wround = 0;
     int wstep = steps, wbuf = 0, wtile = 0;
     i32x4 wr{0, 0, 0, 0x00020000};
     uint32_t woff[S::kWLoads] = {};
@@ -279,8 +279,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
     const auto begin_weights = [&]() {
         if (wstep == steps) {
             wstep = 0;
-            const int64_t t = tile_number(wround++);
-            if (t < total) {
+            const int t = tile_number(wround++);
+            if (t >= 0 && t < total) {
                 find_tile(t, wt);
                 const int64_t base = (int64_t)wt.e * wrows + wt.n0;
                 wr = buffer_of(static_cast<const char *>(a.w) + base * kbytes,
@@ -698,6 +698,8 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
     const int64_t cols = GATED ? kBN / 2 : kBN;
     const int64_t most = (a.n_rows / BM + a.L) * ((a.N + cols - 1) / cols);  // tiles there can be
     const int64_t blocks = most < a.cus ? most : a.cus;
+    if (most + a.cus > 0x7FFFFFFF)
+        return hipErrorInvalidValue;
     hipLaunchKernelGGL((grouped_kernel<MODE, GATED, BM, XBUF, WBUF>), dim3((unsigned)blocks),
                        dim3(kThreads), S::kLds, stream, a);
     return hipGetLastError();
