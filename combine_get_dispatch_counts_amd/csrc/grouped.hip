@@ -16,6 +16,15 @@
 // arrive while this tile's epilogue runs. One barrier per
 // step: it publishes the step's data and tells that the buffer to be loaded
 // next has been read by every wave.
+//
+// Bound by: with few rows the weights from HBM (256 experts of 4096 x 7168
+// codes, 4 rows each, FP8 gated: 1300 us, 5.7 TB/s); with many the loads into
+// LDS beside the matrix unit (29 811 rows of 8 experts, 7168 x 2048 weights,
+// bf16: 770 us, 1.14 PFLOP/s; 49 152 rows of 64 experts, 4096 x 2048, FP8: 483
+// us, 1.71 PFLOP/s): the same launches take 693 and 443 us with the loads
+// alone and 632 and 411 us with the products alone, and 160 KB of LDS leave
+// room for one step ahead at this tile size, too little for the L2's misses
+// (all rows in the L2: 532 and 291 us).
 #include "experts_device.h"
 
 namespace epx {
@@ -23,18 +32,24 @@ namespace {
 
 // How a step's 128 bytes are multiplied.
 //  kBf16: 64 channels, two 16x16x32 bf16 instructions per pair of operands.
-//  kFp8:  128 channels, one 16x16x128 instruction; its sum of 8 products each
-//         is aligned to the largest of them with about 16 bits (measured:
-//         1.5e-5 of the result's spread), below the bf16 rounding of the result.
+//  kFp8:  128 channels, one 16x16x128 instruction. It cuts each product towards
+//         zero to a multiple of 2^(m - 13), m the largest exponent sum of the
+//         products of eight neighbouring channels (measured; the tests hold it
+//         to that), and adds in fp32: a result is off by about 1e-5 of its
+//         products' magnitudes, 7 * 2^-13 of each eight's largest at most.
+//         Taken for the twice as fast instruction: the e4m3 operands have
+//         been rounded by up to 2^-4 each, and the result is rounded to bf16.
 //  kWide: FP8 codes widened to bf16 (exact) in registers, four bf16
 //         instructions, whose sums are full fp32: for the gated FP8 form,
-//         whose scales are fp32 results.
+//         whose scales are fp32 results (with kFp8 they were off by 1.2e-5;
+//         it would take 1540 us in place of 2230 for 256 experts of 128 rows).
 enum Mode { kBf16, kFp8, kWide };
 
 constexpr int kBN = 256;   // weight rows of a tile
 constexpr int kWaves = 8, kThreads = kWaves * kWave;
 constexpr int kWM = 2, kWN = 4;          // wave grid: rows x weight rows
 constexpr int kRow = 128;                // bytes of a row in LDS
+constexpr int kMostTiles = 0x7FFF0000;   // of a call: tile numbers go a few grids past them
 constexpr uint32_t kNowhere = 0xFFFFFF00u;  // a buffer offset past every range: reads as zero
 
 template <Mode MODE, bool GATED, int BM, int XBUF, int WBUF>
@@ -200,23 +215,27 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         }
         if (bad && blockIdx.x == 0)
             flag_error(a.err, EPX_DEV_OVERFLOW);
-        n = (n + BM - 1) / BM;
+        n = n / BM + (n % BM != 0);
         const int incl = wave_inclusive_sum(n);
         if (lane == 63)
             wave_tiles[wave] = incl;
         __syncthreads();
+        // offsets that overlap can name more tiles than 32 bits hold: such
+        // totals stop at kMost (a wave's own total stays below 2^30 + 64)
+        constexpr int kMost = 0x38000000;
         int before = 0;
         for (int w = 0; w < wave; ++w)
-            before += wave_tiles[w];
+            before = min(before + wave_tiles[w], kMost);
         if (tid < a.L)
-            tiles_before[tid + 1] = before + incl;
+            tiles_before[tid + 1] = min(before + incl, kMost);
         if (tid == 0)
             tiles_before[0] = 0;
         __syncthreads();
     }
     constexpr int kCols = GATED ? kBN / 2 : kBN;  // output columns of a tile
     const int nt = (a.N + kCols - 1) / kCols;
-    const int total = uniform(tiles_before[a.L]) * nt;  // below 2^31: checked by the launcher
+    // (what valid offsets can reach is checked by the launcher)
+    const int total = uniform((int)min((int64_t)tiles_before[a.L] * nt, (int64_t)kMostTiles));
     const int wrows = GATED ? 2 * a.N : a.N;
     const int kb_n = a.K >> 7, nb_n = (wrows + 127) >> 7;
     const int64_t kbytes = (int64_t)a.K * S::kEsize;
@@ -280,7 +299,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         if (wstep == steps) {
             wstep = 0;
             const int t = tile_number(wround++);
-            if (t >= 0 && t < total) {
+            if (t < total) {
                 find_tile(t, wt);
                 const int64_t base = (int64_t)wt.e * wrows + wt.n0;
                 wr = buffer_of(static_cast<const char *>(a.w) + base * kbytes,
@@ -698,7 +717,7 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
     const int64_t cols = GATED ? kBN / 2 : kBN;
     const int64_t most = (a.n_rows / BM + a.L) * ((a.N + cols - 1) / cols);  // tiles there can be
     const int64_t blocks = most < a.cus ? most : a.cus;
-    if (most + a.cus > 0x7FFFFFFF)
+    if (most > kMostTiles)
         return hipErrorInvalidValue;
     hipLaunchKernelGGL((grouped_kernel<MODE, GATED, BM, XBUF, WBUF>), dim3((unsigned)blocks),
                        dim3(kThreads), S::kLds, stream, a);
@@ -708,12 +727,13 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
 // Tile height and buffers by the rows an expert has on average (regions: by
 // the rows they hold), which is all the host knows. Few rows: the weights'
 // stream decides, and three steps of both operands in LDS keep more of it
-// under way (256 regions of 4 rows, FP8 gated: 1270 us, against 1510 for 160
+// under way (256 regions of 4 rows, FP8 gated: 1300 us, against 1580 for 160
 // rows with two steps of rows and three of weights). Around 128 rows: one
-// tile per expert (gated FP8, 256 experts of 128 rows: 2230 us, against 2960
-// for 128-row tiles; bf16 has room for three steps of 160 rows: 336 us for 94
-// rows on average, against 371). Many: the fewest bytes per product (bf16,
-// 3700 rows: 780 us against 830; FP8, 770 rows: 500 against 540).
+// tile per expert (gated FP8, 256 experts of 128 rows: 2230 us, against 2900
+// for 128-row tiles; product over regions of 128 rows: 41 against 54; bf16 has
+// room for three steps of 160 rows: 345 us for 94 rows on average, against
+// 362 for 128-row tiles). Many: the fewest bytes per product (bf16, 3700 rows: 770
+// us against 830 for 160-row tiles; FP8, 770 rows: 483 against 517).
 template <Mode MODE, bool GATED>
 hipError_t pick(const GroupedArgs &a, hipStream_t stream)
 {

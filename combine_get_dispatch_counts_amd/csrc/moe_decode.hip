@@ -8,7 +8,13 @@
 // HBM-bound, every weight byte read once, and the matrix instructions only
 // keep the arithmetic out of the way. FP8 weights are widened to bf16 in
 // registers (exact) and their block scales applied to the fp32 sums of 128
-// channels; the tokens stay in bf16.
+// channels; the tokens stay in bf16, and so do the activations between the
+// launches: what grouped_swiglu writes for bf16 rows, and the operand of the
+// second product either way.
+//
+// Measured, first + second launch: FP8, h 7168, f 2048, top-8: 1 token 46 + 33
+// us, 48 tokens over 128 experts 696 + 416 us (5.0 TB/s); bf16, h 4096, f 1536,
+// 8 tokens of top-6 over 64 experts 156 + 85 us.
 //
 // A wave owns 16 weight rows (the A operand of D = W X^T) and a share of the
 // channels; its expert's tokens are the B operand, up to 32 at a time: a
@@ -97,7 +103,7 @@ __device__ __forceinline__ void group_entries(const DecodeArgs &a, Groups &g)
     __syncthreads();
 }
 
-// Sixteen e4m3 codes (two registers' worth of each half) as bf16 operands of eight.
+// Eight e4m3 codes as one bf16 operand.
 __device__ __forceinline__ i32x4 widen8(int lo, int hi)
 {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -6,6 +6,11 @@ may have, for the GPU tests. Every bound is derived, none is fitted:
  * a sum of K exact products in fp32, in any order and with truncating adds,
    is off by at most K 2^-23 times the sum of the products' magnitudes; the
    FP8 form multiplies by two scales and adds again, covered by K + 8;
+ * the plain FP8 product's instruction cuts each product towards zero to a
+   multiple of 2^(m - 13), m the largest exponent sum of the eight products
+   of channels 8 i .. 8 i + 7 (subnormal codes have exponent -6): the largest
+   is kept whole (its last bit is 2^(m - 6)), each of the seven others loses
+   less than 2^(m - 13) (cut below; cut_product is the cut sum itself);
  * exp2 and the reciprocal are within an ulp, the argument of exp2 is rounded
    once: (8 + |g|) 2^-23 of silu(g) u.
 """
@@ -62,6 +67,27 @@ def weights64(w, ws=None):
 def product(x, w):
     """x [m, k] @ w [n, k].T in 64 bits and the fp32 sum's bound."""
     return x @ w.T, (x.shape[1] + 8) * U32 * (x.abs() @ w.abs().T)
+
+
+def cut(x, xs, w, ws):
+    """What cutting can take from the sums of x's rows [m, k] with one expert's
+    rows w [n, k] (codes and scales): 7 times 2^-13 of each eight's largest."""
+    big = lambda v: v.abs().clamp(min=2.0 ** -6).view(v.shape[0], -1, 8).amax(-1)  # noqa: E731
+    k = x.shape[1]
+    gx = big(x.view(torch.float8_e4m3fn).double()) * xs[:, :k // 128].double().repeat_interleave(16, 1)
+    one = torch.full_like(w, 0x38)                                 # codes of 1: the scales
+    gw = big(w.view(torch.float8_e4m3fn).double()) * weights64(one, ws)[:, ::8]
+    return 7 * 2.0 ** -13 * (gx @ gw.T)
+
+
+def cut_product(x, w):
+    """Row i of x times row i of w, codes [n, 128], each product cut."""
+    x, w = (c.view(torch.float8_e4m3fn).double() for c in (x, w))
+    p = (x * w).view(-1, 16, 8)
+    m = sum(torch.floor(torch.log2(c.abs().clamp(min=2.0 ** -6))) for c in (x, w)).view(-1, 16, 8)
+    m = torch.where(p == 0, torch.full_like(m, -99.0), m).amax(-1, keepdim=True)
+    step = 2.0 ** (m - 13)
+    return (torch.trunc(p / step) * step).sum((1, 2)), p.abs().sum((1, 2))
 
 
 def gated(x, w):

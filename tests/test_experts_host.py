@@ -76,3 +76,19 @@ def test_reference_scales():
     assert (v[:128] == 0.5).all() and (v[128:] == 0.25).all()
     with pytest.raises(AssertionError):       # a wrong value is found
         X.assert_close(torch.tensor([1.0]), torch.tensor([1.1]), torch.tensor([0.05]), "planted")
+
+
+def test_reference_cut():
+    """256 * 256 beside a product of 8: 8 is the last bit kept (2^16 / 2^13)."""
+    one = torch.zeros((4, 128), dtype=torch.float8_e4m3fn)
+    x, w = one.clone(), one.clone()
+    x[:, 0] = w[:, 0] = 256.0
+    x[:, 1], w[:, 1] = 2.0, torch.tensor([4.0, 7.5, -7.5, 3.5]).to(torch.float8_e4m3fn)
+    x[:, 8], w[:, 8] = 1.0, 0.5                     # another eight: whole
+    y, mag = X.cut_product(x.view(torch.uint8), w.view(torch.uint8))
+    assert y.tolist() == [65544.5, 65544.5, 65528.5, 65536.5]
+    assert mag[1] == 65551.5
+    c = X.cut(x.view(torch.uint8), torch.full((4, X.stride(128)), 2.0), w.view(torch.uint8),
+              torch.full((1, 1), 3.0))
+    # the first eight, the second (1 * 0.5), fourteen of zeros (2^-6 each)
+    assert abs(float(c[0, 0]) - 6 * 7 * 2.0 ** -13 * (65536 + 0.5 + 14 * 2.0 ** -12)) < 1e-9

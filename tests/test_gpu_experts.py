@@ -1,6 +1,8 @@
 """The experts' arithmetic on the GPU -- weight quantiser, grouped products,
 gated products, low-latency regions, the whole layer for a few tokens --
 against 64-bit results on the CPU within derived bounds (tests/_experts.py)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -105,6 +107,8 @@ def _check_rows(gated, fp8, out, out_s, rows_of, x, xs, w, ws):
         we = X.weights64(w[e], None if ws is None else ws[e])
         if not gated:
             y, tol = X.product(xe, we)
+            if fp8:
+                tol = tol + X.cut(x[r], xs[r], w[e], ws[e])
         else:
             y, tol = X.gated(xe, we)
             if fp8:
@@ -179,6 +183,65 @@ def test_grouped_many_tiles(fp8, gated):
     rng = np.random.default_rng(5)
     counts = [int(c) for c in rng.integers(0, 190, 24)] + [900, 1]
     _run(gated, fp8, counts, 2176, 256, 41)
+
+
+TALL = {
+    # heights of a tile, one row less and one more; on average above 384 rows
+    "tall": [256, 257, 1023, 0, 511],
+    "medium": [159, 160, 161, 321, 97],
+    "short": [127, 128, 129, 1, 0, 31],
+}
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("which", list(TALL))
+def test_grouped_tile_heights(which, gated, fp8):
+    N, K = (384, 640) if fp8 else (264, 200)
+    say(f"grouped {which} gated={gated} fp8={fp8}")
+    _run(gated, fp8, TALL[which], N, K, 43, lead=2, tail=7)
+
+
+@pytest.mark.parametrize("fp8,K", [(False, 64), (False, 40), (False, 128), (True, 128)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows", [70, 150, 500])
+def test_grouped_one_step_many_tiles(rows, gated, fp8, K):
+    """One or two steps of channels, several tiles a block: the loads run more
+    tiles ahead than a tile has steps."""
+    say(f"grouped rows={rows} K={K} gated={gated} fp8={fp8}")
+    rng = np.random.default_rng(6)
+    counts = [int(c) for c in rng.integers(rows - 60, rows + 60, 16)]
+    _run(gated, fp8, counts, 5120 if rows < 200 else 2688, K, 44)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("N,K", [(128, 65536), (65536, 128)])
+def test_grouped_largest_sizes(N, K, fp8):
+    say(f"grouped N={N} K={K} fp8={fp8}")
+    for gated in (False, True):
+        _run(gated, fp8, [2, 0, 17], N, K, 45, lead=1)
+
+
+def test_fp8_products_are_cut_as_stated():
+    """The plain FP8 product against sums of products that are cut the way
+    its instruction cuts them: random codes, and pairs that cancel beside
+    small products."""
+    say("fp8 sums")
+    n, K = 512, 128
+    g = torch.Generator().manual_seed(46)
+    for scale in (110.0, 4.0, 0.02):
+        x = (torch.randn((n, K), generator=g) * 110).clamp(-448, 448)
+        w = (torch.randn((n, K), generator=g) * scale).clamp(-448, 448)
+        x[::2, 1::8], w[::2, 1::8] = -x[::2, ::8], w[::2, ::8]      # cancel in every second row
+        x[::2, 2::8] /= 64
+        x, w = (v.to(torch.float8_e4m3fn).view(torch.uint8) for v in (x, w))
+        off = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        out = epx().grouped_gemm(gpu(x), gpu(w[None]), off,
+                                 torch.ones((n, X.stride(K)), device=DEV),
+                                 torch.ones((1, n // 128, 1), device=DEV))
+        y, mag = X.cut_product(x, w)
+        tol = (K + 8) * X.U32 * mag
+        X.assert_close(out.diagonal(), y, tol + X.BF16 * (y.abs() + tol), f"scale {scale}")
 
 
 # --------------------------------------------------- low-latency regions
@@ -319,6 +382,37 @@ def test_bad_offsets_are_flagged_and_clamped():
     assert untouched(buf, torch.arange(30, 94, device=DEV))
 
 
+def test_size_limits():
+    """What the kernels cannot address is refused before any launch: the
+    pointers are never followed."""
+    from combine_get_dispatch_counts_amd import _lib
+    from combine_get_dispatch_counts_amd.api import _ctx
+
+    say("size limits")
+    lib, ctx, p = _lib.load(), _ctx(DEV), ctypes.c_void_p(256)
+
+    def gemm(n, K, L, N, fp8):
+        return lib.epx_grouped_gemm(ctx, p, p, n, K, p, p, L, N, fp8, p, p, None)
+
+    def swiglu(n, K, L, f, fp8):
+        return lib.epx_grouped_swiglu(ctx, p, p, n, K, p, p, L, f, fp8, p, p, p, None)
+
+    def ll(K, N, fp8, R, cap, L=1):
+        return lib.epx_ll_grouped_gemm(ctx, p, p, K, p, p, L, N, fp8, p, R, cap, p, None)
+
+    for bad in ((1, 65536, 1, 32768, 0), (1, 65536, 1, 65536, 1), (1, 65536 + 128, 1, 8, 0),
+                (1, 8, 1, 65536 + 8, 0), (2 ** 31, 8, 1, 8, 0), (-1, 8, 1, 8, 0), (1, 8, 0, 8, 0),
+                (1, 8, 513, 8, 0)):
+        assert gemm(*bad) == -1, bad
+    for bad in ((1, 65536, 1, 16384, 0), (1, 65536, 1, 32768, 1)):
+        assert swiglu(*bad) == -1, bad
+    assert ll(8192, 8, 0, 64, 8192) == -1            # 8.6 GB of one expert's rows
+    assert ll(65536, 8, 1, 2, 32000) == -1           # with the scales above 4 GB
+    assert ll(8, 8, 0, 65, 1) == -1 and ll(8, 8, 0, 0, 1) == -1 and ll(8, 8, 0, 1, 0) == -1
+    assert ll(8, 8, 0, 64, 65536, L=512) == -1       # 2^31 rows
+    assert epx().get_error() == 0
+
+
 def test_refusals():
     say("refusals")
     m = epx()
@@ -453,6 +547,13 @@ def _check_decode(x, idx, top, w13, w2, **kw):
 def test_moe_decode(T, K, E, h, f, fp8):
     say(f"decode T={T} K={K} E={E} h={h} f={f} fp8={fp8}")
     _check_decode(*_decode_inputs(T, K, E, h, f, fp8, 91 + T))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("h,f", [(65536, 128), (128, 65536)])
+def test_moe_decode_largest_sizes(h, f, fp8):
+    say(f"decode h={h} f={f} fp8={fp8}")
+    _check_decode(*_decode_inputs(3, 2, 2, h, f, fp8, 96))
 
 
 @pytest.mark.parametrize("h,f", [(8, 8), (72, 24), (264, 1000), (1000, 136)])
@@ -625,6 +726,39 @@ def test_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(one, two) and torch.equal(one, three)
     assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+def test_two_streams_at_once():
+    """Different calls of the same operators side by side: nothing is shared."""
+    say("two streams")
+    m = epx()
+    sets = []
+    for seed in (161, 162):
+        x, idx, top, w13, w2 = _layer_inputs(60, 4, 16, 512, 256, seed)
+        xd, id_, td, a, b = gpu(x, idx, top, w13, w2)
+        d = m.dispatch(xd, id_, td, 16, 4)
+        sets.append((xd, id_, td, a, b, d))
+
+    def layer(xd, id_, td, a, b, d):
+        act, _ = m.grouped_swiglu(d.recv_x, a, d.layout.exp_off)
+        return (m.quantize_weights(a)[0], act, m.grouped_gemm(act, b, d.layout.exp_off),
+                m.moe_decode(xd, id_, td, a, b))
+
+    want = [layer(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(6):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(layer(*sets[i]))
+    torch.cuda.synchronize()
+    n = [int(s[5].layout.exp_off[-1]) for s in sets]
+    for i in range(2):
+        for g in got[i]:
+            for j, (u, v) in enumerate(zip(g, want[i])):
+                live = slice(0, n[i]) if j in (1, 2) else slice(None)
+                assert torch.equal(u[live], v[live]), (i, j)
 
 
 def test_graph_replays_follow_the_inputs():
