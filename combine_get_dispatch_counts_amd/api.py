@@ -609,11 +609,12 @@ def quantize_weights(w: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | N
     if K % 128:
         raise EpxError(_lib.EPX_EUNSUPPORTED, f"FP8 weights need K % 128 == 0 (K = {K})")
     if out is None:
-        out = (torch.empty((E, N, K), dtype=torch.uint8, device=dev),
-               torch.empty((E, -(-N // 128), K // 128), dtype=torch.float32, device=dev))
-    codes, scales = out
-    _need(codes, torch.uint8, "codes", shape=(E, N, K), device=dev)
-    _need(scales, torch.float32, "scales", shape=(E, -(-N // 128), K // 128), device=dev)
+        codes = w.new_empty((E, N, K), dtype=torch.uint8)
+        scales = w.new_empty((E, -(-N // 128), K // 128), dtype=torch.float32)
+    else:
+        codes, scales = out
+        _need(codes, torch.uint8, "codes", shape=(E, N, K), device=dev)
+        _need(scales, torch.float32, "scales", shape=(E, -(-N // 128), K // 128), device=dev)
     check(_lib.load().epx_quantize_weights(_ctx(dev), _p(w), E, N, K, _p(codes), _p(scales),
                                            _stream(dev)), "epx_quantize_weights")
     return codes, scales
@@ -629,8 +630,9 @@ def _grouped_operands(x, w, x_scales, w_scales, gated: bool):
     _need(x, dt, "x", 2)
     _need(w, dt, "w", 3, device=dev)
     n, K = x.shape
-    L, rows_w, _ = w.shape
-    _need(w, dt, "w", shape=(L, rows_w, K))
+    L, rows_w, K_w = w.shape
+    if K_w != K:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected {(L, rows_w, K)}")
     if gated and rows_w % 2:
         raise ValueError("w must hold the gate rows, then as many up rows")
     if fp8:
@@ -643,13 +645,16 @@ def _grouped_operands(x, w, x_scales, w_scales, gated: bool):
 
 
 def _swiglu_out(n: int, f: int, fp8: bool, out, out_scales, dev):
+    dt = torch.uint8 if fp8 else torch.bfloat16
     if out is None:
-        out = torch.empty((n, f), dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)
-    _need(out, torch.uint8 if fp8 else torch.bfloat16, "out", shape=(n, f), device=dev)
+        out = torch.empty((n, f), dtype=dt, device=dev)
+    else:
+        _need(out, dt, "out", shape=(n, f), device=dev)
     if fp8:
         if out_scales is None:
             out_scales = torch.empty((n, scale_stride(f)), dtype=torch.float32, device=dev)
-        _need(out_scales, torch.float32, "out_scales", shape=(n, scale_stride(f)), device=dev)
+        else:
+            _need(out_scales, torch.float32, "out_scales", shape=(n, scale_stride(f)), device=dev)
     elif out_scales is not None:
         raise ValueError("out_scales goes with FP8 operands (uint8 codes)")
     return out, out_scales
@@ -668,7 +673,8 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, exp_off: torch.Tensor,
     _need(exp_off, torch.int32, "exp_off", shape=(L + 1,), device=dev)
     if out is None:
         out = torch.empty((n, N), dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, "out", shape=(n, N), device=dev)
+    else:
+        _need(out, torch.bfloat16, "out", shape=(n, N), device=dev)
     check(_lib.load().epx_grouped_gemm(_ctx(dev), _p(x), _p(x_scales), n, K, _p(w), _p(w_scales),
                                        L, N, int(fp8), _p(exp_off), _p(out), _stream(dev)),
           "epx_grouped_gemm")
@@ -714,7 +720,8 @@ def ll_grouped_gemm(x: torch.Tensor, w: torch.Tensor, ll_count: torch.Tensor, ca
     R_buf = _ll_regions(n, L, ll_count, cap, dev)
     if out is None:
         out = torch.empty((n, N), dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, "out", shape=(n, N), device=dev)
+    else:
+        _need(out, torch.bfloat16, "out", shape=(n, N), device=dev)
     check(_lib.load().epx_ll_grouped_gemm(_ctx(dev), _p(x), _p(x_scales), K, _p(w), _p(w_scales),
                                           L, N, int(fp8), _p(ll_count), R_buf, cap, _p(out),
                                           _stream(dev)), "epx_ll_grouped_gemm")
@@ -773,12 +780,14 @@ def moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tens
     elif w13_scales is not None or w2_scales is not None:
         raise ValueError("scales go with FP8 weights (uint8 codes)")
     if out is None:
-        out = torch.empty((T, h), dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, "out", shape=(T, h), device=dev)
+        out = torch.empty_like(x)
+    else:
+        _need(out, torch.bfloat16, "out", shape=(T, h), device=dev)
     if workspace is None:
-        workspace = torch.empty(max(moe_decode_workspace(T, K, f), 16), dtype=torch.uint8,
-                                device=dev)
-    ws_bytes = _nbytes(workspace, dev)
+        ws_bytes = max(moe_decode_workspace(T, K, f), 16)
+        workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
+    else:
+        ws_bytes = _nbytes(workspace, dev)
     check(_lib.load().epx_moe_decode(_ctx(dev), _p(x), h, _p(topk_idx), _p(topk_weights), T, K, E,
                                      _p(w13), _p(w13_scales), _p(w2), _p(w2_scales), f, int(fp8),
                                      _p(workspace), ws_bytes, _p(out), _stream(dev)),
