@@ -754,7 +754,7 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
 // under way (256 regions of 4 rows, FP8 gated: 1300 us, against 1580 for 160
 // rows with two steps of rows and three of weights). Around 128 rows: one
 // tile per expert (gated FP8, 256 experts of 128 rows: 2230 us, against 2900
-// for 128-row tiles; product over regions of 128 rows: 41 against 54; bf16 has
+// for 128-row tiles; product over regions of 128 rows: 34 against 52; bf16 has
 // room for three steps of 160 rows: 345 us for 94 rows on average, against
 // 362 for 128-row tiles). Many: the fewest bytes per product (bf16, 3700 rows: 770
 // us against 830 for 160-row tiles; FP8, 770 rows: 483 against 517).
