@@ -18,7 +18,7 @@
 // next has been read by every wave.
 //
 // Bound by: with few rows the weights from HBM (256 experts of 4096 x 7168
-// codes, 4 rows each, FP8 gated: 1300 us, 5.7 TB/s); with many the loads into
+// codes, 4 rows each, FP8 gated: 1230 us, 6.0 TB/s); with many the loads into
 // LDS beside the matrix unit (29 811 rows of 8 experts, 7168 x 2048 weights,
 // bf16: 770 us, 1.14 PFLOP/s; 49 152 rows of 64 experts, 4096 x 2048, FP8: 483
 // us, 1.71 PFLOP/s): the same launches take 693 and 443 us with the loads
@@ -484,12 +484,20 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
         }
         const char *const sc = smem + S::kScaleAt + group * S::kScale + (s & 3) * 4;
         const char *const xb = xlane + xcur * S::kXStep, *const wb = wlane + wcur * S::kWStep;
-        Raw x = Raw::read(xb, pos);
+        // A wave without rows widens no weights, which would hold up its
+        // neighbour (128-row tiles, 256 regions of four rows: 1230 us against
+        // 1330). Not in the others: 64-row tiles 1235 against 1280 for four rows
+        // an expert but 1380 against 1335 for thirty, 160-row tiles 1% slower.
+        const bool busy = MODE != kWide || BM != 128 || mf > 0;
+        Raw x{};
         Frag<MODE> w[4];
+        if (busy) {
+            x = Raw::read(xb, pos);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = Frag<MODE>(Raw::read(wb + ((j >> 1) * kPairRows + (j & 1) * 4) * kRow,
-                                        pos));
+            for (int j = 0; j < 4; ++j)
+                w[j] = Frag<MODE>(Raw::read(wb + ((j >> 1) * kPairRows + (j & 1) * 4) * kRow,
+                                            pos));
+        }
         float sw[2] = {0.0f, 0.0f};
         if constexpr (S::kFp8Rows) {
             sw[0] = *reinterpret_cast<const float *>(sc + (S::kScaleRows + (GATED ? 0 : wn >> 1)) * 16);
@@ -589,7 +597,10 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
                 if (p >= piece_at(i0))
                     load_piece(p);
         };
-        part(Const<0>{}, Const<2>{});
+        if (busy)
+            part(Const<0>{}, Const<2>{});
+        else
+            rest(0);
         if (MF > 2 && mf > 2) {
             part(Const<(MF > 2 ? 2 : 0)>{}, Const<2>{});
             if (MF > 4 && mf > 4) {
@@ -601,7 +612,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(GroupedArgs a)
             } else if (MF > 4) {
                 rest(4);
             }
-        } else if (MF > 2) {
+        } else if (MF > 2 && busy) {
             rest(2);
         }
         end_rows();
@@ -751,8 +762,12 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
 // Tile height and buffers by the rows an expert has on average (regions: by
 // the rows they hold), which is all the host knows. Few rows: the weights'
 // stream decides, and three steps of both operands in LDS keep more of it
-// under way (256 regions of 4 rows, FP8 gated: 1300 us, against 1580 for 160
-// rows with two steps of rows and three of weights). Around 128 rows: one
+// under way (256 regions of 4 rows, FP8 gated: 1230 us, against 1580 for 160
+// rows with two steps of rows and three of weights); with at most 64, or 48 on
+// average, 64-row tiles load less that is not used (8 experts of 16 rows,
+// 4096 x 1024, bf16 gated: 15.3 us, against 22.3 for 160-row tiles; FP8 gated,
+// 64 experts of 32 rows, 4096 x 2048: 107, against 112 for 128-row tiles).
+// Around 128 rows: one
 // tile per expert (gated FP8, 256 experts of 128 rows: 2230 us, against 2900
 // for 128-row tiles; product over regions of 128 rows: 34 against 52; bf16 has
 // room for three steps of 160 rows: 345 us for 94 rows on average, against
@@ -766,6 +781,8 @@ hipError_t pick(const GroupedArgs &a, hipStream_t stream)
         if (a.off && per > 384)
             return launch<MODE, GATED, 256, 2, 2>(a, stream);
     }
+    if (per <= (a.off ? 48 : 64))
+        return launch<MODE, GATED, 64, 3, 3>(a, stream);
     if constexpr (MODE == kBf16)
         return launch<MODE, GATED, 160, 3, 3>(a, stream);
     else

@@ -249,7 +249,8 @@ def test_fp8_products_are_cut_as_stated():
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("L,R,cap,most", [(1, 1, 1, 1), (5, 1, 33, 33), (3, 4, 20, 20),
-                                          (2, 64, 9, 4), (300, 1, 3, 3), (2, 8, 100, 100)])
+                                          (2, 64, 9, 4), (300, 1, 3, 3), (2, 8, 100, 100),
+                                          (3, 1, 128, 12), (3, 1, 128, 128), (4, 2, 64, 20)])
 def test_ll_grouped(L, R, cap, most, gated, fp8):
     say(f"ll grouped L={L} R={R} cap={cap} gated={gated} fp8={fp8}")
     N, K = 256, 384
