@@ -12,9 +12,10 @@
 // launches: what grouped_swiglu writes for bf16 rows, and the operand of the
 // second product either way.
 //
-// Measured, first + second launch: FP8, h 7168, f 2048, top-8: 1 token 46 + 33
-// us, 48 tokens over 128 experts 696 + 416 us (5.0 TB/s); bf16, h 4096, f 1536,
-// 8 tokens of top-6 over 64 experts 156 + 85 us.
+// Measured, per call (first + second launch, traced): FP8, h 7168, f 2048,
+// top-8: 1 token 80 us (48 + 35), 48 tokens over 128 experts 1120 us, 4.9 TB/s
+// (731 + 447); bf16, h 4096, f 1536, 8 tokens of top-6 over 64 experts 233 to
+// 250 us (162 + 89).
 //
 // A wave owns 16 weight rows (the A operand of D = W X^T) and a share of the
 // channels; its expert's tokens are the B operand, up to 32 at a time: a
@@ -116,8 +117,8 @@ __device__ __forceinline__ i32x4 widen8(int lo, int hi)
 }
 
 // No nontemporal hint: a fragment's rows are read in two halves of a 128-byte
-// line, and with the hint the second half came from memory again (up launch
-// at 48 tokens 837 us against 696).
+// line, and with the hint the second half came from memory again (first
+// launch, 48 tokens: 837 us against 696 when it was tried).
 __device__ __forceinline__ i32x4 load_weights(const char *p)
 {
     return *reinterpret_cast<const i32x4 *>(p);
