@@ -81,16 +81,21 @@ struct Shape {
 };
 
 // 64 lanes x 16 bytes from a buffer into LDS at lds (wave-uniform), lane l's
-// bytes at lds + 16 l. Not tracked by the compiler: wait with wait_loads.
+// bytes at lds + 16 l. Not tracked by the compiler: wait with wait_and_meet.
+// A vector memory instruction may read a scalar register no earlier than five
+// wait states after a vector instruction wrote it (v_readfirstlane for the
+// descriptor, v_readlane where one was spilled), and the compiler does not
+// look inside the block: the block's first two instructions are those five,
+// and the one that m0 needs.
 __device__ __forceinline__ void load_lds(uint32_t lds, i32x4 rsrc, uint32_t voff, uint32_t soff)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         rsrc[i] = __builtin_amdgcn_readfirstlane(rsrc[i]);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                      lds),
                  "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // Wait until at most N of the wave's memory operations are under way, and
