@@ -38,9 +38,14 @@ __device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b)
 }
 
 // silu(g) * u = g / (1 + exp(-g)) * u in fp32. exp as 2^(-g log2 e) and the
-// reciprocal are the hardware's, each within an ulp: a few 1e-7 relative,
-// far below the bf16 or e4m3 rounding that follows. exp overflows to
-// infinity for g below -88, where the quotient is zero.
+// reciprocal are the hardware's, each within an ulp; the argument of 2^x and
+// the constant in it are rounded, which the exponential multiplies by g. Off
+// by at most (8 + |g|) 2^-23 of the value: 5e-7 near zero, some 6e-6 for g =
+// -80 (for g > 0 the exponential vanishes beside 1). Far below the bf16 or
+// e4m3 rounding that follows, and as an error of the FP8 form's fp32 scales
+// only where silu itself has gone to nothing. Below g = -87.3 the reciprocal,
+// and below -88.7 the exponential's inverse, leave fp32's normal range: the
+// quotient, 1e-36 at most, is zero.
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
     const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);

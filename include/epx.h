@@ -476,7 +476,9 @@ int epx_grouped_gemm(epx_ctx *ctx, const void *x, const float *x_scales, int64_t
  * w [L, 2f, K]: rows 0 .. f-1 of an expert are its gate, f .. 2f-1 its up
  * projection (w_scales [L, 2f/128, K/128] with fp8).
  * Out: with g and u the products in fp32 (the FP8 form's whole: nothing is
- *      dropped), a = g / (1 + exp(-g)) * u.
+ *      dropped), a = g / (1 + exp(-g)) * u, within (8 + |g|) 2^-23 of itself
+ *      before its rounding; the quotient is zero for g below -87.3, where it
+ *      is less than 1e-36.
  *      fp8 = 0: out [n_rows, f] bf16 (f a multiple of 8; out_scales NULL).
  *      fp8 = 1: out [n_rows, f] e4m3 codes and out_scales [n_rows,
  *      epx_scale_stride(f)], one scale per row and 128 columns in
