@@ -33,7 +33,10 @@ def _ctx(device: torch.device) -> ctypes.c_void_p:
 
 def _stream(device: torch.device) -> ctypes.c_void_p:
     idx = device.index if device.index is not None else torch.cuda.current_device()
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(idx))
+    # the handle alone takes a fraction of a Stream object's time (some 1 us a
+    # call less), but is not a public name of torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return ctypes.c_void_p(raw(idx) if raw else torch.cuda.current_stream(idx).cuda_stream)
 
 
 def _p(t: torch.Tensor | None) -> ctypes.c_void_p | None:
