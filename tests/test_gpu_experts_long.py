@@ -247,3 +247,24 @@ def test_fp8_layer_against_the_same_roundings(ll):
     say(f"relative error {rel(out, want):.5f}, few tokens {rel(few, want_few[:64]):.5f}")
     assert rel(out, want) <= 2 * X.BF16
     assert rel(few, want_few[:64]) <= 2 * X.BF16
+
+
+def test_gates_where_silu_leaves_fp32():
+    """Gates around -88 beside huge up values: the stated error down to where
+    the quotient is said to be zero, zero from there on."""
+    say("gates around -88")
+    gates = torch.tensor([-60.0, -80.0, -86.0, -87.0, -87.5, -88.0, -88.5, -89.0, -100.0, -3e38])
+    n, K, N = len(gates), 8, 8
+    x = torch.zeros((n, K))
+    x[:, 0], x[:, 1] = gates, 1.0
+    w = torch.zeros((1, 2 * N, K))
+    w[0, :N, 0], w[0, N:, 1] = 1.0, 2.0 ** 100
+    off = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    act, _ = epx().grouped_swiglu(gpu(x.to(torch.bfloat16)), gpu(w.to(torch.bfloat16)), off)
+    assert epx().get_error() == 0
+    act = act.cpu().float()
+    assert (act[4:] == 0).all(), act[:, 0]
+    g = x[:4, :1].to(torch.bfloat16).double()
+    a = g / (1 + torch.exp(-g)) * 2.0 ** 100
+    a, tol = a.expand(4, N), ((8 + g.abs()) * X.U32 * a.abs()).expand(4, N)
+    X.assert_close(act[:4], a, tol + X.BF16 * (a.abs() + tol), "gates above -87.3")
