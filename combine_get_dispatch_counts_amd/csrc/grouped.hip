@@ -17,14 +17,16 @@
 // step: it publishes the step's data and tells that the buffer to be loaded
 // next has been read by every wave.
 //
-// Bound by: with few rows the weights from HBM (256 experts of 4096 x 7168
-// codes, 4 rows each, FP8 gated: 1230 us, 6.0 TB/s); with many the loads into
-// LDS beside the matrix unit (29 811 rows of 8 experts, 7168 x 2048 weights,
-// bf16: 770 us, 1.14 PFLOP/s; 49 152 rows of 64 experts, 4096 x 2048, FP8: 483
-// us, 1.71 PFLOP/s): the same launches take 693 and 443 us with the loads
-// alone and 632 and 411 us with the products alone, and 160 KB of LDS leave
-// room for one step ahead at this tile size, too little for the L2's misses
-// (all rows in the L2: 532 and 291 us).
+// Bound by: with few rows the weights from HBM (256 regions of 4 rows, 4096 x
+// 7168 codes, FP8 gated: 1231 us, 6.0 TB/s). With many, the products and the
+// loads beside them (49 152 rows of 64 experts, 4096 x 2048 weights, FP8: 490
+// us, 1.68 PFLOP/s; 29 811 rows of 8 experts, 7168 x 2048, bf16: 783 us, 1.12
+// PFLOP/s): without loads behind the first steps the same launches take 361
+// and 567 us, the loads alone 324 and 552, and both with all operands in the
+// L2 434 and 717. The matrix unit is busy for 40% and 54% of the time: every
+// step begins with fragment reads behind its barrier, and at this tile size
+// 160 KB of LDS leave room for one step of loads ahead, too little for the
+// L2's misses.
 #include "experts_device.h"
 
 namespace epx {
@@ -42,7 +44,7 @@ namespace {
 //  kWide: FP8 codes widened to bf16 (exact) in registers, four bf16
 //         instructions, whose sums are full fp32: for the gated FP8 form,
 //         whose scales are fp32 results (with kFp8 they were off by 1.2e-5;
-//         it would take 1540 us in place of 2230 for 256 experts of 128 rows).
+//         256 experts of 128 rows took 1540 us with it, and take 2330).
 enum Mode { kBf16, kFp8, kWide };
 
 constexpr int kBN = 256;   // weight rows of a tile
@@ -764,20 +766,21 @@ hipError_t launch(const GroupedArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Tile height and buffers by the rows an expert has on average (regions: by
-// the rows they hold), which is all the host knows. Few rows: the weights'
-// stream decides, and three steps of both operands in LDS keep more of it
-// under way (256 regions of 4 rows, FP8 gated: 1230 us, against 1580 for 160
-// rows with two steps of rows and three of weights); with at most 64, or 48 on
-// average, 64-row tiles load less that is not used (8 experts of 16 rows,
-// 4096 x 1024, bf16 gated: 15.3 us, against 22.3 for 160-row tiles; FP8 gated,
-// 64 experts of 32 rows, 4096 x 2048: 107, against 112 for 128-row tiles).
-// Around 128 rows: one
-// tile per expert (gated FP8, 256 experts of 128 rows: 2230 us, against 2900
-// for 128-row tiles; product over regions of 128 rows: 34 against 52; bf16 has
-// room for three steps of 160 rows: 345 us for 94 rows on average, against
-// 362 for 128-row tiles). Many: the fewest bytes per product (bf16, 3700 rows: 770
-// us against 830 for 160-row tiles; FP8, 770 rows: 483 against 517).
+// Tile height and buffers by the rows an expert has on average, as far as the
+// host knows them: n_rows / L, for regions their capacity, however few rows
+// they hold. (The pairs of times are from when each choice was made.) Few
+// rows: the weights' stream decides, and three steps of both operands in LDS
+// keep more of it under way (256 regions of 4 rows, FP8 gated: capacity 128
+// 1237 us; capacity 129 and more, 160 rows with two steps of rows and three of
+// weights, 1598); with at most 64, or 48 on average, 64-row tiles load less
+// that is not used (8 experts of 16 rows, 4096 x 1024, bf16 gated: 15.3 us,
+// against 22.3 for 160-row tiles; FP8 gated, 64 experts of 32 rows, 4096 x 2048:
+// 107, against 112 for 128-row tiles). Around 128 rows: one tile per expert
+// (gated FP8, 256 experts of 128 rows: 2230 us, against 2900 for 128-row
+// tiles; product over regions of 128 rows: 34 against 52; bf16 has room for
+// three steps of 160 rows: 345 us for 94 rows on average, against 362 for
+// 128-row tiles). Many: the fewest bytes per product (bf16, 3700 rows: 770 us
+// against 830 for 160-row tiles; FP8, 770 rows: 483 against 517).
 template <Mode MODE, bool GATED>
 hipError_t pick(const GroupedArgs &a, hipStream_t stream)
 {

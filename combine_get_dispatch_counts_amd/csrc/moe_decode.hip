@@ -4,18 +4,23 @@
 //   out[t]  = bf16( sum_k topw[t, k] * (W2 a[t, k]) )
 //
 // With few tokens each expert's weights serve a handful of rows, so both
-// launches are streams over the weights of the experts that were routed to:
-// HBM-bound, every weight byte read once, and the matrix instructions only
-// keep the arithmetic out of the way. FP8 weights are widened to bf16 in
-// registers (exact) and their block scales applied to the fp32 sums of 128
-// channels; the tokens stay in bf16, and so do the activations between the
-// launches: what grouped_swiglu writes for bf16 rows, and the operand of the
-// second product either way.
+// launches are streams over the weights of the experts that were routed to: a
+// weight is read once for every 32 tokens of its expert, and the matrix
+// instructions only keep the arithmetic out of the way. FP8 weights are widened
+// to bf16 in registers (exact) and their block scales applied to the fp32 sums
+// of 128 channels; the tokens stay in bf16, and so do the activations between
+// the launches: what grouped_swiglu writes for bf16 rows, and the operand of
+// the second product either way (the result is off by 0.0023 of its norm in
+// place of 0.0017 with fp32 activations).
 //
-// Measured, per call (first + second launch, traced): FP8, h 7168, f 2048,
-// top-8: 1 token 80 us (48 + 35), 48 tokens over 128 experts 1120 us, 4.9 TB/s
-// (731 + 447); bf16, h 4096, f 1536, 8 tokens of top-6 over 64 experts 233 to
-// 250 us (162 + 89).
+// Measured per call, back to back: FP8, h 7168, f 2048, top-8: 1 token 80 us,
+// 48 tokens over 128 experts 1130 us, 4.8 TB/s; bf16, h 4096, f 1536, 8 tokens
+// of top-6 over 64 experts 229 to 250 us. First and second launch in a kernel
+// trace, which lengthens them by some percent: 49 + 35, 731 + 445 (4.9 and 4.0
+// TB/s), 162 + 89. The second launch's grid is one block per 16 columns of h
+// and knows nothing of the device: 448 blocks for h = 7168, but 64 for h = 1024,
+// whose experts then stream through 64 of 256 compute units (32 tokens of
+// top-8, 256 experts, f 4096: 858 us a call, 2.5 TB/s).
 //
 // A wave owns 16 weight rows (the A operand of D = W X^T) and a share of the
 // channels; its expert's tokens are the B operand, up to 32 at a time: a

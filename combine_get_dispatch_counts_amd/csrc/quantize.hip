@@ -6,7 +6,7 @@
 // have one block, 32 rows each: lane l holds channels 16 (l % 8) .. + 15 of
 // rows l / 8 + 8 p in registers, so w is read once, and only the largest
 // magnitudes meet, in LDS. HBM-bound (2 bytes read and 1 written per weight):
-// 32 matrices of 4096 x 7168 in 513 us, 5.5 TB/s; 96 blocks, latency, 4.3 us
+// 32 matrices of 4096 x 7168 in 515 us, 5.5 TB/s; 96 blocks, latency, 4.3 us
 // (one wave a block: 2 us more, and 20% slower on large matrices whose rows are
 // a power of two apart). The loads have no nontemporal hint: a lane's 32 bytes
 // are two loads, and with it half a line came from memory twice (542 us).
