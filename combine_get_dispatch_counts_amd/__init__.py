@@ -10,14 +10,21 @@ run before it exists.)
 from ._lib import EpxError
 
 from .api import (  # noqa: E402
+    Balance,
     Dispatched,
     Layout,
     LowLatency,
+    Normed,
+    alloc_balance,
     alloc_dispatch,
     alloc_layout,
     alloc_ll,
+    alloc_norm,
+    balance_loss,
+    balance_workspace,
     calibrate_sweep_rate,
     combine,
+    combine_backward,
     combine_final,
     combine_partial,
     dispatch,
@@ -40,6 +47,11 @@ from .api import (  # noqa: E402
     quantize_weights,
     Received,
     recv_permute,
+    rms_norm,
+    rms_norm_backward,
+    rms_norm_backward_workspace,
+    route,
+    route_backward,
     scale_stride,
     set_sweep_rate,
     workspace_size,
@@ -52,4 +64,7 @@ __all__ = ["EpxError", "Layout", "Dispatched", "LowLatency", "workspace_size", "
            "ll_dispatch", "Received", "recv_permute", "fused_workspace_size",
            "fused_launches", "dispatch_fused", "set_sweep_rate", "get_sweep_rate",
            "calibrate_sweep_rate", "quantize_weights", "grouped_gemm", "grouped_swiglu",
-           "ll_grouped_gemm", "ll_grouped_swiglu", "moe_decode_workspace", "moe_decode"]
+           "ll_grouped_gemm", "ll_grouped_swiglu", "moe_decode_workspace", "moe_decode", "Normed",
+           "alloc_norm", "rms_norm", "rms_norm_backward_workspace", "rms_norm_backward", "route",
+           "Balance", "alloc_balance", "balance_workspace", "balance_loss", "route_backward",
+           "combine_backward"]

@@ -11,15 +11,17 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libepx.so")
 
 EPX_OK, EPX_EINVAL, EPX_ECAPACITY, EPX_EUNSUPPORTED, EPX_EHIP, EPX_EDEVICE = 0, -1, -2, -3, -4, -5
-DEV_BAD_ROUTE, DEV_OVERFLOW, DEV_BAD_HANDLE, DEV_WORKSPACE = 1, 2, 4, 8
+DEV_BAD_ROUTE, DEV_OVERFLOW, DEV_BAD_HANDLE, DEV_WORKSPACE, DEV_BAD_LOGIT = 1, 2, 4, 8, 16
 MAX_TOPK, MAX_EXPERTS, MAX_RANKS, MAX_SWEEP_GBPS = 32, 512, 64, 100000
 NOALLOC_SCRATCH_BYTES = 1 << 20
 MAX_CHANNELS, MAX_DECODE_TOKENS, MAX_EXPERT_BYTES = 65536, 64, 0xFFFF0000
+MAX_NORM_CHANNELS = 32768
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 # name -> (restype, argtypes); the order follows include/epx.h
 SIGNATURES = {
@@ -54,6 +56,14 @@ SIGNATURES = {
     "epx_moe_decode_workspace": (_SZ, [_I, _I, _I]),
     "epx_moe_decode": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _SZ, _P,
                             _P]),
+    "epx_rms_norm": (_I, [_P, _P, _P, _P, _I, _I, _I, _F] + [_P] * 5),
+    "epx_rms_norm_backward_workspace": (_SZ, [_I, _I]),
+    "epx_rms_norm_backward": (_I, [_P] * 4 + [_I, _P, _I, _I, _F, _P, _SZ, _P, _P, _P]),
+    "epx_route": (_I, [_P] * 4 + [_I] * 7 + [_F, _P, _P, _P]),
+    "epx_balance_workspace": (_SZ, [_I, _I, _I]),
+    "epx_balance_loss": (_I, [_P] * 4 + [_I] * 5 + [_P] * 5 + [_SZ, _P]),
+    "epx_route_backward": (_I, [_P] * 3 + [_I] * 5 + [_F] + [_P] * 5 + [_I, _P, _P]),
+    "epx_combine_backward": (_I, [_P, _P, _P, _I64, _I, _P, _P, _I, _I, _P, _P, _P]),
     "epx_get_error": (_I, [_P, ctypes.POINTER(_I), _P]),
 }
 

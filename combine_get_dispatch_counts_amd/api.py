@@ -798,6 +798,310 @@ def moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tens
     return out
 
 
+def _weight(w: torch.Tensor, h: int, dev: torch.device) -> int:
+    """1 if the norm's weight is fp32, 0 if bf16."""
+    f32 = w is not None and w.dtype == torch.float32
+    _need(w, torch.float32 if f32 else torch.bfloat16, "weight", shape=(h,), device=dev)
+    return int(f32)
+
+
+@dataclass
+class Normed:
+    out: torch.Tensor | None = None       # [T,h] bf16
+    residual: torch.Tensor | None = None  # [T,h] bf16: x + residual
+    codes: torch.Tensor | None = None     # [T,h] uint8, e4m3 codes
+    scales: torch.Tensor | None = None    # [T, scale_stride(h)] fp32
+
+
+def alloc_norm(T: int, h: int, residual: bool, bf16: bool, fp8: bool,
+               device: torch.device) -> Normed:
+    rows = dict(dtype=torch.bfloat16, device=device)
+    return Normed(
+        out=torch.empty((T, h), **rows) if bf16 else None,
+        residual=torch.empty((T, h), **rows) if residual else None,
+        codes=torch.empty((T, h), dtype=torch.uint8, device=device) if fp8 else None,
+        scales=torch.empty((T, scale_stride(h)), dtype=torch.float32,
+                           device=device) if fp8 else None)
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: torch.Tensor | None = None, bf16: bool = True, fp8: bool = False,
+             buf: Normed | None = None) -> Normed:
+    """y = v / sqrt(mean(v^2) + eps) * weight per row of v = x + residual (x
+    alone without one), x and residual [T,h] bf16, weight [h] bf16 or fp32.
+    Returns v in bf16 (``residual``, where one was given), y in bf16 (``out``,
+    with ``bf16``) and y as FP8 rows in dispatch's format (``codes`` and
+    ``scales``, with ``fp8``), what grouped_gemm and grouped_swiglu read. ``buf``
+    (alloc_norm's, or any tensors of those shapes) avoids allocating and says
+    by its members which outputs there are; its residual may be ``residual``
+    or ``x`` itself, and its out one of them that its residual is not."""
+    _need(x, torch.bfloat16, "x", 2)
+    dev = x.device
+    T, h = x.shape
+    f32 = _weight(weight, h, dev)
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual", shape=(T, h), device=dev)
+    if buf is None:
+        buf = alloc_norm(T, h, residual is not None, bf16, fp8, dev)
+    else:
+        if residual is not None:
+            _need(buf.residual, torch.bfloat16, "buf.residual", shape=(T, h), device=dev)
+        elif buf.residual is not None:
+            raise ValueError("buf.residual goes with a residual")
+        if buf.out is not None:
+            _need(buf.out, torch.bfloat16, "buf.out", shape=(T, h), device=dev)
+        if buf.codes is not None:
+            _need(buf.codes, torch.uint8, "buf.codes", shape=(T, h), device=dev)
+            _need(buf.scales, torch.float32, "buf.scales", shape=(T, scale_stride(h)), device=dev)
+        elif buf.scales is not None:
+            raise ValueError("buf.scales goes with buf.codes")
+    if buf.out is None and buf.codes is None:
+        raise ValueError("rms_norm needs out or codes to write")
+    check(_lib.load().epx_rms_norm(_ctx(dev), _p(x), _p(residual), _p(weight), f32, T, h, eps,
+                                   _p(buf.residual), _p(buf.out), _p(buf.codes), _p(buf.scales),
+                                   _stream(dev)), "epx_rms_norm")
+    return buf
+
+
+def rms_norm_backward_workspace(T: int, h: int) -> int:
+    return int(_lib.load().epx_rms_norm_backward_workspace(T, h))
+
+
+def rms_norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                      eps: float = 1e-6, dresidual: torch.Tensor | None = None,
+                      out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                      workspace: torch.Tensor | None = None
+                      ) -> tuple[torch.Tensor, torch.Tensor]:
+    """rms_norm's gradient: (dx [T,h] bf16, dweight [h] fp32) from dout [T,h]
+    bf16 and x [T,h] bf16, what was normed (rms_norm's ``residual`` where it
+    had one). ``dresidual`` [T,h] bf16, the gradient that reaches that sum by
+    its other ways, is added to dx, which is the gradient of rms_norm's x and
+    of its residual alike. ``out`` (dx, dweight; dx may be dout or dresidual)
+    and ``workspace`` (rms_norm_backward_workspace(T, h) bytes; calls that
+    share one must not overlap) avoid allocating."""
+    _need(x, torch.bfloat16, "x", 2)
+    dev = x.device
+    T, h = x.shape
+    _need(dout, torch.bfloat16, "dout", shape=(T, h), device=dev)
+    f32 = _weight(weight, h, dev)
+    if dresidual is not None:
+        _need(dresidual, torch.bfloat16, "dresidual", shape=(T, h), device=dev)
+    if out is None:
+        dx, dweight = torch.empty_like(x), x.new_empty(h, dtype=torch.float32)
+    else:
+        dx, dweight = out
+        _need(dx, torch.bfloat16, "dx", shape=(T, h), device=dev)
+        _need(dweight, torch.float32, "dweight", shape=(h,), device=dev)
+    if workspace is None:
+        ws_bytes = max(rms_norm_backward_workspace(T, h), 16)
+        workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
+    else:
+        ws_bytes = _nbytes(workspace, dev)
+    check(_lib.load().epx_rms_norm_backward(_ctx(dev), _p(dout), _p(x), _p(weight), f32,
+                                            _p(dresidual), T, h, eps, _p(workspace), ws_bytes,
+                                            _p(dx), _p(dweight), _stream(dev)),
+          "epx_rms_norm_backward")
+    return dx, dweight
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _scoring(name: str) -> int:
+    if name not in _SCORING:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {name!r}")
+    return _SCORING[name]
+
+
+def route(logits: torch.Tensor, topk: int, scoring: str = "softmax",
+          bias: torch.Tensor | None = None, num_groups: int = 1, topk_groups: int = 1,
+          normalize: bool = True, scale: float = 1.0, mask: torch.Tensor | None = None,
+          out: tuple[torch.Tensor, torch.Tensor] | None = None
+          ) -> tuple[torch.Tensor, torch.Tensor]:
+    """The router's choice: (topk_idx [T,topk] int64, topk_weights [T,topk]
+    fp32) from logits [T,E] fp32, as dispatch, moe_decode and combine read
+    them. Scores are the softmax or the sigmoids of the logits; the experts
+    of the largest score + ``bias`` ([E] fp32, for the choice alone) are
+    taken, largest first, ties to the lower expert; the weights are their
+    scores, over their sum with ``normalize``, times ``scale``. With
+    ``num_groups`` > 1 only the experts of the ``topk_groups`` best groups
+    (sum of the two best) can be chosen. A logit of -inf keeps an expert
+    from being chosen; ``mask`` [T] bool (or uint8) is False for padding,
+    which gets -1 and 0 everywhere, as entries do for which no expert is
+    left. ``out`` (topk_idx, topk_weights) avoids allocating."""
+    _need(logits, torch.float32, "logits", 2)
+    dev = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, "bias", shape=(E,), device=dev)
+    if mask is not None:
+        _need(mask, torch.uint8 if mask.dtype == torch.uint8 else torch.bool, "mask", shape=(T,),
+              device=dev)
+    if out is None:
+        idx = logits.new_empty((T, topk), dtype=torch.int64)
+        w = logits.new_empty((T, topk))
+    else:
+        idx, w = out
+        _need(idx, torch.int64, "topk_idx", shape=(T, topk), device=dev)
+        _need(w, torch.float32, "topk_weights", shape=(T, topk), device=dev)
+    check(_lib.load().epx_route(_ctx(dev), _p(logits), _p(bias), _p(mask), T, E, topk,
+                                _scoring(scoring), num_groups, topk_groups, int(normalize), scale,
+                                _p(idx), _p(w), _stream(dev)), "epx_route")
+    return idx, w
+
+
+@dataclass
+class Balance:
+    loss: torch.Tensor        # [1] fp32
+    counts: torch.Tensor      # [S,E] int32: entries per expert
+    probs: torch.Tensor       # [S,E] fp32: mean share per expert
+    num_tokens: torch.Tensor  # [S+1] int32: tokens that count, then sequences that have any
+
+
+def alloc_balance(S: int, E: int, device: torch.device) -> Balance:
+    return Balance(loss=torch.empty(1, dtype=torch.float32, device=device),
+                   counts=torch.empty((S, E), dtype=torch.int32, device=device),
+                   probs=torch.empty((S, E), dtype=torch.float32, device=device),
+                   num_tokens=torch.empty(S + 1, dtype=torch.int32, device=device))
+
+
+def balance_workspace(T: int, E: int, S: int) -> int:
+    return int(_lib.load().epx_balance_workspace(T, E, S))
+
+
+def _sequences(seq_off: torch.Tensor | None, dev: torch.device) -> int:
+    if seq_off is None:
+        return 1
+    _need(seq_off, torch.int32, "seq_off", 1, device=dev)
+    if seq_off.numel() < 2:
+        raise ValueError("seq_off needs an entry per sequence and one more")
+    return seq_off.numel() - 1
+
+
+def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, scoring: str = "softmax",
+                 seq_off: torch.Tensor | None = None, out: Balance | None = None,
+                 workspace: torch.Tensor | None = None) -> Balance:
+    """Balance loss, per-expert counts and mean shares of logits [T,E] fp32 and
+    topk_idx [T,K] int64 (-1: no route; tokens without any do not count). Per
+    sequence of n tokens loss_s = E / (K n) * sum over experts of counts *
+    probs; the loss is the mean over the sequences that have tokens.
+    ``seq_off`` int32 [S+1]: the sequences' first tokens, and where the last
+    ends (None: one sequence of all tokens). ``out`` (alloc_balance) and
+    ``workspace`` (balance_workspace(T, E, S) bytes; calls that share one must
+    not overlap) avoid allocating."""
+    _need(logits, torch.float32, "logits", 2)
+    dev = logits.device
+    T, E = logits.shape
+    _need(topk_idx, torch.int64, "topk_idx", 2, device=dev)
+    K = topk_idx.shape[1]
+    _need(topk_idx, torch.int64, "topk_idx", shape=(T, K))
+    S = _sequences(seq_off, dev)
+    if out is None:
+        out = alloc_balance(S, E, dev)
+    else:
+        _check_balance(out, S, E, dev)
+        _need(out.loss, torch.float32, "loss", shape=(1,), device=dev)
+        _need(out.probs, torch.float32, "probs", shape=(S, E), device=dev)
+    if workspace is None:
+        ws_bytes = max(balance_workspace(T, E, S), 16)
+        workspace = logits.new_empty(ws_bytes, dtype=torch.uint8)
+    else:
+        ws_bytes = _nbytes(workspace, dev)
+    check(_lib.load().epx_balance_loss(_ctx(dev), _p(logits), _p(topk_idx), _p(seq_off), T, E, K, S,
+                                       _scoring(scoring), _p(out.loss), _p(out.counts),
+                                       _p(out.probs), _p(out.num_tokens), _p(workspace), ws_bytes,
+                                       _stream(dev)), "epx_balance_loss")
+    return out
+
+
+def _check_balance(b: Balance, S: int, E: int, dev: torch.device) -> None:
+    _need(b.counts, torch.int32, "counts", shape=(S, E), device=dev)
+    _need(b.num_tokens, torch.int32, "num_tokens", shape=(S + 1,), device=dev)
+
+
+def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, scoring: str = "softmax",
+                   normalize: bool = True, scale: float = 1.0,
+                   dtopk_weights: torch.Tensor | None = None, balance: Balance | None = None,
+                   dloss: torch.Tensor | None = None, seq_off: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient with respect to the logits (dlogits [T,E] fp32) of route's
+    weights (``dtopk_weights`` [T,K] fp32, as combine_backward gives it), of
+    the balance loss (``balance`` as balance_loss left it, ``dloss`` [1] fp32
+    on the device, and the ``seq_off`` it was given), or of both in one pass.
+    logits, topk_idx, scoring, normalize and scale as in the forward calls;
+    the choice and the counts are constants. ``out`` avoids allocating."""
+    _need(logits, torch.float32, "logits", 2)
+    dev = logits.device
+    T, E = logits.shape
+    _need(topk_idx, torch.int64, "topk_idx", 2, device=dev)
+    K = topk_idx.shape[1]
+    _need(topk_idx, torch.int64, "topk_idx", shape=(T, K))
+    if dtopk_weights is None and balance is None:
+        raise ValueError("route_backward needs dtopk_weights, balance or both")
+    if dtopk_weights is not None:
+        _need(dtopk_weights, torch.float32, "dtopk_weights", shape=(T, K), device=dev)
+    S = 1
+    if balance is not None:
+        S = _sequences(seq_off, dev)
+        _check_balance(balance, S, E, dev)
+        _need(dloss, torch.float32, "dloss", device=dev)
+        if dloss.numel() != 1:
+            raise ValueError(f"dloss has {dloss.numel()} entries, expected 1")
+    elif dloss is not None or seq_off is not None:
+        raise ValueError("dloss and seq_off go with balance")
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _need(out, torch.float32, "out", shape=(T, E), device=dev)
+    counts, seen = (balance.counts, balance.num_tokens) if balance is not None else (None, None)
+    check(_lib.load().epx_route_backward(_ctx(dev), _p(logits), _p(topk_idx), T, E, K,
+                                         _scoring(scoring), int(normalize), scale,
+                                         _p(dtopk_weights), _p(counts), _p(seen), _p(dloss),
+                                         _p(seq_off), S, _p(out), _stream(dev)),
+          "epx_route_backward")
+    return out
+
+
+def combine_backward(dout: torch.Tensor, expert_out: torch.Tensor | None, pos: torch.Tensor,
+                     topk_weights: torch.Tensor,
+                     out: tuple[torch.Tensor | None, torch.Tensor | None] | None = None
+                     ) -> tuple[torch.Tensor | None, torch.Tensor | None]:
+    """combine's gradient: (d_expert_out [rows,h] bf16, d_topk_weights [T,K]
+    fp32) from dout [T,h] bf16 and what combine was given. Rows of
+    d_expert_out that no entry of ``pos`` names are not written. ``out``
+    (either may be None: that gradient is left out) avoids allocating; without
+    d_topk_weights expert_out is not read, but still says how many rows there
+    are (None: as many as out[0] has)."""
+    _need(dout, torch.bfloat16, "dout", 2)
+    dev = dout.device
+    T, h = dout.shape
+    _need(pos, torch.int32, "pos", 2, device=dev)
+    K = pos.shape[1]
+    _need(pos, torch.int32, "pos", shape=(T, K))
+    _need(topk_weights, torch.float32, "topk_weights", shape=(T, K), device=dev)
+    dy, dw = out if out is not None else (None, None)
+    rows_of = dy if expert_out is None else expert_out
+    _need(rows_of, torch.bfloat16, "expert_out", 2, device=dev)
+    n = rows_of.shape[0]
+    _need(rows_of, torch.bfloat16, "expert_out", shape=(n, h))
+    if out is None:
+        dy = torch.empty_like(expert_out)
+        dw = torch.empty_like(topk_weights)
+    else:
+        if dy is None and dw is None:
+            raise ValueError("combine_backward needs an output")
+        if dy is not None:
+            _need(dy, torch.bfloat16, "d_expert_out", shape=(n, h), device=dev)
+        if dw is not None:
+            _need(dw, torch.float32, "d_topk_weights", shape=(T, K), device=dev)
+            if expert_out is None:
+                raise ValueError("d_topk_weights needs expert_out")
+    check(_lib.load().epx_combine_backward(_ctx(dev), _p(dout), _p(expert_out), n, h,
+                                           _p(topk_weights), _p(pos), T, K, _p(dy), _p(dw),
+                                           _stream(dev)), "epx_combine_backward")
+    return dy, dw
+
+
 __all__ = ["EpxError", "Layout", "Dispatched", "LowLatency", "workspace_size", "ll_size_hint",
            "scale_stride", "get_error", "alloc_layout", "get_dispatch_layout", "alloc_dispatch",
            "get_dispatch_layout_noalloc", "dispatch", "combine", "combine_partial",
@@ -805,4 +1109,7 @@ __all__ = ["EpxError", "Layout", "Dispatched", "LowLatency", "workspace_size", "
            "ll_dispatch", "Received", "recv_permute", "fused_workspace_size",
            "fused_launches", "dispatch_fused", "set_sweep_rate", "get_sweep_rate",
            "calibrate_sweep_rate", "quantize_weights", "grouped_gemm", "grouped_swiglu",
-           "ll_grouped_gemm", "ll_grouped_swiglu", "moe_decode_workspace", "moe_decode"]
+           "ll_grouped_gemm", "ll_grouped_swiglu", "moe_decode_workspace", "moe_decode", "Normed",
+           "alloc_norm", "rms_norm", "rms_norm_backward_workspace", "rms_norm_backward", "route",
+           "Balance", "alloc_balance", "balance_workspace", "balance_loss", "route_backward",
+           "combine_backward"]

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libepx.so")
 SOURCES = ["epx_api.hip", "layout.hip", "dispatch.hip", "combine.hip", "fused.hip",
-           "quantize.hip", "grouped.hip", "moe_decode.hip"]
+           "quantize.hip", "grouped.hip", "moe_decode.hip", "norm.hip", "route.hip",
+           "combine_backward.hip"]
 ARCH = "gfx950"
 
 

@@ -13,6 +13,7 @@
 #include "epx.h"
 #include "epx_internal.h"
 #include "experts_internal.h"
+#include "gate_internal.h"
 
 namespace {
 
@@ -832,6 +833,185 @@ int epx_moe_decode(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_i
     a.T = T; a.K = K; a.E = E; a.h = h; a.f = f;
     a.act = static_cast<uint16_t *>(ws); a.out = out; a.err = ctx->d_err; a.cus = ctx->cus;
     return launched(epx::launch_moe_decode(a, fp8 != 0, stream));
+}
+
+// h of a norm's rows.
+static int check_norm(int T, int h, float eps, int fp8)
+{
+    if (T < 0 || h > EPX_MAX_NORM_CHANNELS || !(eps >= 0.0f) || eps > 3.0e38f)
+        return EPX_EINVAL;
+    return check_hidden(h, fp8);
+}
+
+int epx_rms_norm(epx_ctx *ctx, const uint16_t *x, const uint16_t *residual, const void *weight,
+                 int weight_fp32, int T, int h, float eps, uint16_t *residual_out, uint16_t *out,
+                 uint8_t *codes, float *scales, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if ((rc = check_norm(T, h, eps, codes != nullptr)) != EPX_OK)
+        return rc;
+    if (T > 0) {
+        if (!x || !weight || (!out && !codes) || (codes && !scales) || (scales && !codes) ||
+            (residual && !residual_out) || (residual_out && !residual))
+            return EPX_EINVAL;
+        if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) ||
+            !aligned16(residual_out) || !aligned16(out) || !aligned16(codes) ||
+            !aligned16(scales))
+            return EPX_EINVAL;
+    }
+    epx::NormArgs a{};
+    a.x = x; a.residual = residual; a.w = weight; a.T = T; a.h = h; a.eps = eps;
+    a.res_out = residual_out; a.out = out; a.codes = codes; a.scales = scales;
+    return launched(epx::launch_rms_norm(a, weight_fp32 != 0, stream));
+}
+
+size_t epx_rms_norm_backward_workspace(int T, int h)
+{
+    if (check_norm(T, h, 0.0f, 0) != EPX_OK)
+        return 0;
+    return (size_t)epx::norm_bwd_blocks(T, h) * h * sizeof(float);
+}
+
+int epx_rms_norm_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *x,
+                          const void *weight, int weight_fp32, const uint16_t *dresidual, int T,
+                          int h, float eps, void *ws, size_t ws_bytes, uint16_t *dx,
+                          float *dweight, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if ((rc = check_norm(T, h, eps, 0)) != EPX_OK)
+        return rc;
+    if (!dweight || !aligned16(dweight))
+        return EPX_EINVAL;
+    if (T > 0) {
+        if (!dout || !x || !weight || !dx || !ws)
+            return EPX_EINVAL;
+        if (!aligned16(dout) || !aligned16(x) || !aligned16(weight) || !aligned16(dresidual) ||
+            !aligned16(dx) || !aligned16(ws))
+            return EPX_EINVAL;
+        if (ws_bytes < epx_rms_norm_backward_workspace(T, h))
+            return EPX_ECAPACITY;
+    }
+    epx::NormBwdArgs a{};
+    a.dout = dout; a.x = x; a.w = weight; a.dres = dresidual; a.T = T; a.h = h; a.eps = eps;
+    a.dx = dx; a.dw = dweight; a.partial = static_cast<float *>(ws);
+    return launched(epx::launch_rms_norm_backward(a, weight_fp32 != 0, stream));
+}
+
+// Sizes of the router's calls; a token's entries are distinct experts only in
+// the choice itself.
+static int check_router(int T, int K, int E, int scoring)
+{
+    if (scoring != EPX_SOFTMAX && scoring != EPX_SIGMOID)
+        return EPX_EINVAL;
+    return check_routing(T, K, E, 1);
+}
+
+int epx_route(epx_ctx *ctx, const float *logits, const float *bias, const uint8_t *mask, int T,
+              int E, int K, int scoring, int num_groups, int topk_groups, int normalize,
+              float scale, int64_t *topk_idx, float *topk_w, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if ((rc = check_router(T, K, E, scoring)) != EPX_OK)
+        return rc;
+    if (K > E || num_groups < 1 || num_groups > 64 || E % num_groups != 0 || topk_groups < 1 ||
+        topk_groups > num_groups || !(scale > -3.0e38f && scale < 3.0e38f))
+        return EPX_EINVAL;
+    if (T > 0 && (!logits || !topk_idx || !topk_w))
+        return EPX_EINVAL;
+    epx::RouteArgs a{};
+    a.logits = logits; a.bias = bias; a.mask = mask;
+    a.T = T; a.E = E; a.K = K;
+    // all groups kept: no limit
+    a.G = topk_groups == num_groups ? 1 : num_groups;
+    a.top_groups = topk_groups; a.group_size = E / num_groups;
+    a.size_mul = epx::div_magic(a.group_size);
+    a.scale = scale; a.topk_idx = topk_idx; a.topk_w = topk_w; a.err = ctx->d_err;
+    return launched(epx::launch_route(a, scoring == EPX_SIGMOID, normalize != 0, stream));
+}
+
+size_t epx_balance_workspace(int T, int E, int S)
+{
+    if (check_routing(T, 1, E, 1) != EPX_OK || S < 1)
+        return 0;
+    return epx::balance_workspace_bytes(T, E, S);
+}
+
+int epx_balance_loss(epx_ctx *ctx, const float *logits, const int64_t *topk_idx,
+                     const int32_t *seq_off, int T, int E, int K, int S, int scoring, float *loss,
+                     int32_t *counts, float *probs, int32_t *num_tokens, void *ws,
+                     size_t ws_bytes, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if ((rc = check_router(T, K, E, scoring)) != EPX_OK)
+        return rc;
+    if (S < 1 || (!seq_off && S != 1) || !loss || !counts || !probs || !num_tokens || !ws ||
+        !aligned16(ws) || (T > 0 && (!logits || !topk_idx)))
+        return EPX_EINVAL;
+    if (ws_bytes < epx_balance_workspace(T, E, S))
+        return EPX_ECAPACITY;
+    epx::BalanceArgs a{};
+    a.logits = logits; a.topk_idx = topk_idx; a.seq_off = seq_off;
+    a.T = T; a.E = E; a.K = K; a.S = S;
+    a.loss = loss; a.counts = counts; a.probs = probs; a.num_tokens = num_tokens;
+    a.ws = ws; a.err = ctx->d_err;
+    return launched(epx::launch_balance(a, scoring == EPX_SIGMOID, stream));
+}
+
+int epx_route_backward(epx_ctx *ctx, const float *logits, const int64_t *topk_idx, int T, int E,
+                       int K, int scoring, int normalize, float scale, const float *dtopk_w,
+                       const int32_t *counts, const int32_t *num_tokens, const float *dloss,
+                       const int32_t *seq_off, int S, float *dlogits, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if ((rc = check_router(T, K, E, scoring)) != EPX_OK)
+        return rc;
+    if (!(scale > -3.0e38f && scale < 3.0e38f) || (!dtopk_w && !counts) ||
+        (counts ? !num_tokens || !dloss || S < 1 || (!seq_off && S != 1)
+                : num_tokens || dloss || seq_off))
+        return EPX_EINVAL;
+    if (T > 0 && (!logits || !topk_idx || !dlogits))
+        return EPX_EINVAL;
+    epx::RouteBwdArgs a{};
+    a.logits = logits; a.topk_idx = topk_idx; a.dtopk_w = dtopk_w;
+    a.counts = counts; a.num_tokens = num_tokens; a.dloss = dloss; a.seq_off = seq_off;
+    a.T = T; a.E = E; a.K = K; a.S = S; a.scale = scale;
+    a.dlogits = dlogits; a.err = ctx->d_err;
+    return launched(epx::launch_route_backward(a, scoring == EPX_SIGMOID, normalize != 0, stream));
+}
+
+int epx_combine_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *expert_out,
+                         int64_t n_rows, int h, const float *topk_w, const int32_t *pos, int T,
+                         int K, uint16_t *d_expert_out, float *d_topk_w, hipStream_t stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc != EPX_OK)
+        return rc;
+    if (T < 0 || K < 1 || K > EPX_MAX_TOPK || n_rows < 0 || n_rows > INT32_MAX ||
+        h > EPX_MAX_CHANNELS || (int64_t)T * K > INT32_MAX)
+        return EPX_EINVAL;
+    if ((rc = check_hidden(h, 0)) != EPX_OK)
+        return rc;
+    if (T > 0) {
+        if (!dout || !topk_w || !pos || (!d_expert_out && !d_topk_w) ||
+            (n_rows > 0 && d_topk_w && !expert_out))
+            return EPX_EINVAL;
+        if (!aligned16(dout) || !aligned16(expert_out) || !aligned16(d_expert_out))
+            return EPX_EINVAL;
+    }
+    epx::CombineBwdArgs a{};
+    a.dout = dout; a.y = expert_out; a.n_rows = n_rows; a.h = h; a.T = T; a.K = K;
+    a.topk_w = topk_w; a.pos = pos; a.dy = d_expert_out; a.dtopk_w = d_topk_w; a.err = ctx->d_err;
+    return launched(epx::launch_combine_backward(a, stream));
 }
 
 int epx_get_error(epx_ctx *ctx, int *device_flags, hipStream_t stream)

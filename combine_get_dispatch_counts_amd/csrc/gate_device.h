@@ -1,0 +1,103 @@
+// gate_device.h -- device helpers of the norm, the choice of experts and the
+// gradients (gfx950): reductions over a wave, the exponential, bf16 vectors.
+#pragma once
+
+#include "epx_device.h"
+#include "gate_internal.h"
+
+namespace epx {
+
+// Reductions over the 64 lanes of a wave with data-parallel-primitive moves
+// (no LDS): sums and maxima of 16 lanes by shifts within a row, then the rows
+// joined by two broadcasts; lane 63 ends with the whole, which every lane
+// gets. The order of a sum's additions is fixed.
+#define EPX_DPP(v, ident, ctrl, rows) \
+    __builtin_amdgcn_update_dpp((int)(ident), (int)(v), ctrl, rows, 0xF, false)
+
+__device__ __forceinline__ float last_lane(float v)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#define EPX_STEP(ctrl, rows) \
+    v = v + __int_as_float(EPX_DPP(__float_as_int(v), 0, ctrl, rows))
+    EPX_STEP(0x111, 0xF);  // row_shr:1
+    EPX_STEP(0x112, 0xF);
+    EPX_STEP(0x114, 0xF);
+    EPX_STEP(0x118, 0xF);
+    EPX_STEP(0x142, 0xA);  // row_bcast:15 into rows 1 and 3
+    EPX_STEP(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
+#undef EPX_STEP
+    return last_lane(v);
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+#define EPX_STEP(ctrl, rows) v = max(v, (uint32_t)EPX_DPP(v, 0, ctrl, rows))
+    EPX_STEP(0x111, 0xF);
+    EPX_STEP(0x112, 0xF);
+    EPX_STEP(0x114, 0xF);
+    EPX_STEP(0x118, 0xF);
+    EPX_STEP(0x142, 0xA);
+    EPX_STEP(0x143, 0xC);
+#undef EPX_STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Largest of each 16 adjacent lanes, in all 16 of them.
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    v = max(v, (uint32_t)EPX_DPP(v, 0, 0x128, 0xF));  // row_ror:8
+    v = max(v, (uint32_t)EPX_DPP(v, 0, 0x124, 0xF));
+    v = max(v, (uint32_t)EPX_DPP(v, 0, 0x122, 0xF));
+    return max(v, (uint32_t)EPX_DPP(v, 0, 0x121, 0xF));
+}
+
+// fp32 values as unsigned numbers in the same order; 0 lies below them all
+// (-inf maps to 0x007FFFFF). NaN is not ordered here.
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float unordered(uint32_t o)
+{
+    return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+
+// exp(x) in fp32 within two units of the last place for results in the normal
+// range: the hardware's 2^t (one unit) at t = x log2 e, and the part of the
+// product that its rounding drops -- up to |x| 2^-24 of the result -- put back
+// as a factor. Below -200 the result is 0, as it is from -104 on.
+__device__ __forceinline__ float exp_fp32(float x)
+{
+    x = fmaxf(x, -200.0f);
+    const float t = x * 0x1.715476p+0f;
+    const float r = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -t));
+    return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, 0x1.62e43p-1f, 1.0f);
+}
+
+__device__ __forceinline__ void widen8(const u32x4 &p, float (&f)[8])
+{
+    const uint32_t e[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(e[i]);
+        f[2 * i + 1] = bf16_hi(e[i]);
+    }
+}
+
+__device__ __forceinline__ u32x4 narrow8(const float (&f)[8])
+{
+    u32x4 o;
+    o.x = f32_to_bf16(f[0]) | (f32_to_bf16(f[1]) << 16);
+    o.y = f32_to_bf16(f[2]) | (f32_to_bf16(f[3]) << 16);
+    o.z = f32_to_bf16(f[4]) | (f32_to_bf16(f[5]) << 16);
+    o.w = f32_to_bf16(f[6]) | (f32_to_bf16(f[7]) << 16);
+    return o;
+}
+
+}  // namespace epx

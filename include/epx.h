@@ -61,6 +61,8 @@ extern "C" {
 #define EPX_DEV_BAD_HANDLE 4  /* a combine handle row >= n_rows */
 #define EPX_DEV_WORKSPACE 8   /* the layout workspace was not zeroed before its
                                  first use, or is shared by overlapping calls */
+#define EPX_DEV_BAD_LOGIT 16  /* a NaN or +inf among the router's logits, or NaN
+                                 or +inf in its bias */
 
 /* Limits of this implementation */
 #define EPX_MAX_TOPK 32
@@ -68,6 +70,7 @@ extern "C" {
 #define EPX_MAX_RANKS 64
 #define EPX_MAX_SWEEP_GBPS 100000
 #define EPX_MAX_CHANNELS 65536      /* K, N and f of the experts' products */
+#define EPX_MAX_NORM_CHANNELS 32768 /* h of the norm */
 #define EPX_MAX_DECODE_TOKENS 64    /* T of epx_moe_decode */
 #define EPX_MAX_EXPERT_BYTES 0xFFFF0000ll /* one expert's matrix (w13: both halves) */
 #define EPX_NOALLOC_SCRATCH_BYTES (1u << 20) /* see epx_get_dispatch_layout_noalloc */
@@ -529,6 +532,137 @@ int epx_moe_decode(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_i
                    const float *topk_w, int T, int K, int E, const void *w13,
                    const float *w13_scales, const void *w2, const float *w2_scales, int f,
                    int fp8, void *ws, size_t ws_bytes, uint16_t *out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * In front of the dispatch and behind the combine in training: residual norm,
+ * choice of experts, balance loss, and gradients. Logits, weights of entries,
+ * losses and their gradients are fp32, rows are bf16.
+ * ------------------------------------------------------------------------ */
+
+/* Root-mean-square norm of T rows, with the residual's addition and FP8 rows:
+ * per row, in fp32, v = x + residual (x alone without one),
+ *   y = v / sqrt(mean(v^2) + eps) * weight.
+ * In:  x [T, h] bf16; residual [T, h] bf16 or NULL; weight [h], bf16
+ *      (weight_fp32 = 0) or fp32 (1); eps >= 0.
+ * Out: residual_out [T, h] bf16 = v (with a residual; else NULL); out [T, h]
+ *      bf16 = y, or NULL; codes [T, h] and scales [T, epx_scale_stride(h)] =
+ *      y as FP8 rows in epx_dispatch's format (s = max(amax, 1e-4) / 448 per
+ *      128 channels, code e4m3(y / s), padding +0), or both NULL. At least one
+ *      of out and codes. Every output is rounded once from fp32: y is not made
+ *      from the rounded v, nor the codes from the rounded y.
+ * h a multiple of 8, with codes of 128 (else EPX_EUNSUPPORTED), at most
+ * EPX_MAX_NORM_CHANNELS. Buffers 16-byte aligned. residual_out may be residual or
+ * x, and out may be x or residual where it is not residual_out too; no other
+ * overlap. The squares are summed in fp32: rows with values beyond 1e18 / h
+ * leave its range. A row with an Inf or NaN gives NaN. */
+int epx_rms_norm(epx_ctx *ctx, const uint16_t *x, const uint16_t *residual, const void *weight,
+                 int weight_fp32, int T, int h, float eps, uint16_t *residual_out, uint16_t *out,
+                 uint8_t *codes, float *scales, hipStream_t stream);
+
+/* Workspace bytes of epx_rms_norm_backward (host): partial sums of the
+ * weight's gradient. Returns 0 for bad arguments and for T = 0. */
+size_t epx_rms_norm_backward_workspace(int T, int h);
+
+/* The norm's gradient: with n = x / sqrt(mean(x^2) + eps) and g = dout weight,
+ *   dx = dresidual + (g - n mean(g n)) / sqrt(mean(x^2) + eps),
+ *   dweight = sum over rows of dout n.
+ * In:  dout [T, h] bf16; x [T, h] bf16, what was normed (residual_out where
+ *      the forward pass had a residual); weight as there; dresidual [T, h]
+ *      bf16, the gradient that arrives at residual_out by its other ways, or
+ *      NULL. ws: epx_rms_norm_backward_workspace bytes, 16-byte aligned, no
+ *      initial contents; calls that share it must not overlap.
+ * Out: dx [T, h] bf16, the gradient of x and of the residual alike (it may be
+ *      dout or dresidual, no other overlap); dweight [h] fp32 (zeros if
+ *      T = 0). The same inputs give the same bytes. */
+int epx_rms_norm_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *x,
+                          const void *weight, int weight_fp32, const uint16_t *dresidual, int T,
+                          int h, float eps, void *ws, size_t ws_bytes, uint16_t *dx,
+                          float *dweight, hipStream_t stream);
+
+/* How a logit becomes a score */
+#define EPX_SOFTMAX 0  /* exp(l_e) / sum over the experts of exp(l) */
+#define EPX_SIGMOID 1  /* 1 / (1 + exp(-l_e)) */
+
+/* The router's choice: per token the K experts of the largest s_e + bias_e
+ * (s the score), largest first, ties to the lower expert.
+ * In:  logits [T, E] fp32. -inf: the expert is not live for that token, i.e.
+ *      never chosen and without a share of the softmax. NaN and +inf are taken
+ *      as -inf and set EPX_DEV_BAD_LOGIT. bias [E] fp32 or NULL: counts for
+ *      the choice alone, not for the weights (-inf: never chosen; NaN, +inf:
+ *      the same with EPX_DEV_BAD_LOGIT).
+ *      num_groups G, topk_groups: with G > 1, experts [g E/G, (g+1) E/G) form
+ *      group g (E % G == 0, G <= 64), a group's score is the sum of the two
+ *      largest s_e + bias_e of its live experts (the one there is, if one), and
+ *      only the topk_groups best groups' experts can be chosen (ties to the
+ *      lower group; groups without live experts last). G = 1: no limit.
+ *      mask [T] uint8 or NULL: a token with mask 0 (padding) gets no route.
+ * Out: topk_idx [T, K] int64, -1 where fewer experts can be chosen; topk_w
+ *      [T, K] fp32: scale * s of the chosen, divided by the sum over the
+ *      token's chosen with `normalize`; 0 beside a -1. As epx_dispatch,
+ *      epx_moe_decode and epx_combine read them.
+ * Scores are in fp32 with full relative precision down to their underflow;
+ * normalized weights also below it. The choice is that of the exact scores of
+ * the given logits, computed again in 64 bits where fp32 cannot tell. K <= E
+ * and K <= EPX_MAX_TOPK; rows of no token are not read. */
+int epx_route(epx_ctx *ctx, const float *logits, const float *bias, const uint8_t *mask, int T,
+              int E, int K, int scoring, int num_groups, int topk_groups, int normalize,
+              float scale, int64_t *topk_idx, float *topk_w, hipStream_t stream);
+
+/* Workspace bytes of epx_balance_loss (host). Returns 0 for bad arguments. */
+size_t epx_balance_workspace(int T, int E, int S);
+
+/* Balance loss, per-expert counts and mean shares of S sequences. A token
+ * counts if one of its entries is an expert; p_e = s_e / sum s over its live
+ * experts (softmax: s_e itself). With n the tokens of a sequence that count,
+ * c_e their entries for expert e and P_e the mean of p_e over them,
+ *   loss_s = E / (K n) * sum over e of c_e P_e   (1 if all is even),
+ * and the loss is the mean of loss_s over the sequences with n > 0 (0 if none).
+ * In:  logits [T, E] fp32 as in epx_route; topk_idx [T, K] int64 (-1 = no
+ *      route; others outside [0, E) set EPX_DEV_BAD_ROUTE and are skipped; an
+ *      expert named twice counts twice); seq_off [S+1] int32, sequence s being
+ *      tokens [seq_off[s], seq_off[s+1]), or NULL: one sequence of all T
+ *      (S = 1). Tokens of no sequence do not count. Offsets that decrease or
+ *      leave [0, T] set EPX_DEV_OVERFLOW. ws: epx_balance_workspace bytes,
+ *      16-byte aligned, no initial contents; calls that share it must not
+ *      overlap.
+ * Out: loss [1] fp32; counts [S, E] int32 (c_e); probs [S, E] fp32 (P_e);
+ *      num_tokens [S+1] int32: n of each sequence, then the number of
+ *      sequences with n > 0. Sums are fp32 in a fixed order: the same inputs
+ *      give the same bytes. */
+int epx_balance_loss(epx_ctx *ctx, const float *logits, const int64_t *topk_idx,
+                     const int32_t *seq_off, int T, int E, int K, int S, int scoring, float *loss,
+                     int32_t *counts, float *probs, int32_t *num_tokens, void *ws,
+                     size_t ws_bytes, hipStream_t stream);
+
+/* Gradient with respect to the logits of the weights that epx_route gave, of
+ * the balance loss, or of both at once (the choice and the counts are
+ * constants).
+ * In:  logits, topk_idx, scoring, normalize and scale as there (entries of -1
+ *      have no part; -inf, NaN and +inf logits get 0); dtopk_w [T, K] fp32, the
+ *      gradient of topk_w (entries beside a -1 are not looked at), or NULL;
+ *      counts, num_tokens as epx_balance_loss left them, seq_off and S as
+ *      given to it, and dloss [1] fp32 (device), the gradient of the loss; or
+ *      all NULL (S is then not looked at). At least one of dtopk_w and counts.
+ * Out: dlogits [T, E] fp32, written whole. */
+int epx_route_backward(epx_ctx *ctx, const float *logits, const int64_t *topk_idx, int T, int E,
+                       int K, int scoring, int normalize, float scale, const float *dtopk_w,
+                       const int32_t *counts, const int32_t *num_tokens, const float *dloss,
+                       const int32_t *seq_off, int S, float *dlogits, hipStream_t stream);
+
+/* epx_combine's gradient.
+ * In:  dout [T, h] bf16; expert_out [n_rows, h] bf16, topk_w [T, K] fp32 and
+ *      pos [T, K] as given to epx_combine (no row named twice, as in every
+ *      handle).
+ * Out: d_expert_out [n_rows, h] bf16, or NULL: row pos[t,k] = topk_w[t,k] *
+ *      dout[t], rounded once; rows that no entry names are left as they were.
+ *      d_topk_w [T, K] fp32, or NULL (expert_out may then be NULL too): the
+ *      sum over the channels of dout[t] * expert_out[pos[t,k]] in fp32, in a
+ *      fixed order; 0 where pos < 0. At least one of the two. A handle row >=
+ *      n_rows sets EPX_DEV_BAD_HANDLE and counts as -1. Buffers of rows
+ *      16-byte aligned; outputs must not overlap inputs. */
+int epx_combine_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *expert_out,
+                         int64_t n_rows, int h, const float *topk_w, const int32_t *pos, int T,
+                         int K, uint16_t *d_expert_out, float *d_topk_w, hipStream_t stream);
 
 /* Synchronise `stream`, return the device error word in *device_flags (host)
  * and clear it. Returns EPX_EDEVICE if any bit was set, EPX_OK otherwise. */
