@@ -7,10 +7,8 @@
 
 namespace epx {
 
-// Reductions over the 64 lanes of a wave with data-parallel-primitive moves
-// (no LDS): sums and maxima of 16 lanes by shifts within a row, then the rows
-// joined by two broadcasts; lane 63 ends with the whole, which every lane
-// gets. The order of a sum's additions is fixed.
+// Reductions with data-parallel-primitive moves between lanes (no LDS). The
+// order of a sum's additions is fixed.
 #define EPX_DPP(v, ident, ctrl, rows) \
     __builtin_amdgcn_update_dpp((int)(ident), (int)(v), ctrl, rows, 0xF, false)
 
@@ -19,6 +17,8 @@ __device__ __forceinline__ float last_lane(float v)
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// Over the 64 lanes of a wave: 16 lanes by shifts within a row, the rows joined
+// by two broadcasts; lane 63 ends with the whole, which every lane gets.
 __device__ __forceinline__ float wave_sum(float v)
 {
 #define EPX_STEP(ctrl, rows) \
@@ -33,20 +33,8 @@ __device__ __forceinline__ float wave_sum(float v)
     return last_lane(v);
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
-{
-#define EPX_STEP(ctrl, rows) v = max(v, (uint32_t)EPX_DPP(v, 0, ctrl, rows))
-    EPX_STEP(0x111, 0xF);
-    EPX_STEP(0x112, 0xF);
-    EPX_STEP(0x114, 0xF);
-    EPX_STEP(0x118, 0xF);
-    EPX_STEP(0x142, 0xA);
-    EPX_STEP(0x143, 0xC);
-#undef EPX_STEP
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-
-// Largest of each 16 adjacent lanes, in all 16 of them.
+// Over each 16 adjacent lanes (a row), the result in all 16 of them: rotations
+// pair the same values in every lane, so a sum is the same in each.
 __device__ __forceinline__ uint32_t row_max(uint32_t v)
 {
     v = max(v, (uint32_t)EPX_DPP(v, 0, 0x128, 0xF));  // row_ror:8
@@ -55,17 +43,34 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v)
     return max(v, (uint32_t)EPX_DPP(v, 0, 0x121, 0xF));
 }
 
-// fp32 values as unsigned numbers in the same order; 0 lies below them all
-// (-inf maps to 0x007FFFFF). NaN is not ordered here.
-__device__ __forceinline__ uint32_t ordered(float v)
+__device__ __forceinline__ float row_max(float v)
 {
-    const uint32_t u = __float_as_uint(v);
-    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+#define EPX_STEP(ctrl) v = fmaxf(v, __int_as_float(EPX_DPP(__float_as_int(v), 0, ctrl, 0xF)))
+    EPX_STEP(0x128);
+    EPX_STEP(0x124);
+    EPX_STEP(0x122);
+    EPX_STEP(0x121);
+#undef EPX_STEP
+    return v;
 }
 
-__device__ __forceinline__ float unordered(uint32_t o)
+__device__ __forceinline__ float row_sum(float v)
 {
-    return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+#define EPX_STEP(ctrl) v = v + __int_as_float(EPX_DPP(__float_as_int(v), 0, ctrl, 0xF))
+    EPX_STEP(0x128);
+    EPX_STEP(0x124);
+    EPX_STEP(0x122);
+    EPX_STEP(0x121);
+#undef EPX_STEP
+    return v;
+}
+
+// The row's 16 bits of a ballot.
+__device__ __forceinline__ uint32_t row_ballot(bool b)
+{
+    const uint64_t m = __ballot(b);
+    const int row = lane_id() >> 4;
+    return (uint32_t)((row & 2 ? m >> 32 : m) >> (16 * (row & 1))) & 0xFFFFu;
 }
 
 // exp(x) in fp32 within two units of the last place for results in the normal

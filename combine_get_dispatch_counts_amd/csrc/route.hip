@@ -3,61 +3,84 @@
 //
 // Scores of a token's logits l (an expert is live unless its logit is -inf):
 //   softmax  s_e = exp(l_e) / sum exp(l),   sigmoid  s_e = 1 / (1 + exp(-l_e)),
-// and their shares of one p_e = s_e / sum s (softmax: p = s). A wave has one
-// token; lane i holds the logits of experts V i .. V i + V - 1, so lanes
-// ascend with the experts and the lowest lane that has a value also has the
-// lowest expert that has it.
+// and their shares of one p_e = s_e / sum s (softmax: p = s).
 //
-// The choice is that of the exact scores: fp32 scores decide wherever they
-// are further apart than their error, and a token whose decision falls
-// between nearer ones is done again in 64 bits.
+// A wave has four tokens, 16 lanes (a row of the data-parallel moves) each:
+// sums and maxima over a token's experts take four moves, and instructions
+// that concern a token as a whole serve four. Lane i of a token holds the N
+// logits of experts 4 (i + 16 q) .. + 3, q < N / 4, which are 16-byte pieces
+// of one row, adjacent over the lanes.
 #include "gate_device.h"
 
 namespace epx {
 namespace {
 
 constexpr float kInf = __builtin_inff();
+constexpr int kRow = 16;                  // lanes of a token
+constexpr int kTokens = kWave / kRow;     // tokens of a wave
+
+__device__ __forceinline__ int row_lane() { return threadIdx.x & (kRow - 1); }
+
+// The expert of a lane's j-th logit.
+__device__ __forceinline__ int expert(int j) { return 4 * (row_lane() + kRow * (j >> 2)) + (j & 3); }
+
+// Four values of a row from its element e on, `none` past its end. wide: E % 4
+// == 0 and rows of whole 16-byte pieces.
+template <typename V4, typename V>
+__device__ __forceinline__ V4 load4(const V *row, int e, int E, bool wide, V none)
+{
+    V4 q = {none, none, none, none};
+    if (e < E) {
+        if (wide) {
+            q = *reinterpret_cast<const V4 *>(row + e);
+        } else {
+            q.x = row[e];
+            if (e + 1 < E)
+                q.y = row[e + 1];
+            if (e + 2 < E)
+                q.z = row[e + 2];
+            if (e + 3 < E)
+                q.w = row[e + 3];
+        }
+    }
+    return q;
+}
 
 // A token's logits: -inf where the lane has no expert, and for a NaN or +inf,
 // which sets bad.
-template <int V>
-__device__ __forceinline__ void load_logits(const float *row, int E, bool wide, float (&l)[V],
-                                            bool &bad)
+template <int N>
+__device__ __forceinline__ void load_logits(const float *row, int E, bool wide, bool live,
+                                            float (&l)[N], bool &bad)
 {
-    const int e0 = lane_id() * V;
-    if constexpr (V >= 4) {
-        if (wide && e0 < E) {  // E % 4 == 0 and rows of whole 16-byte pieces
+    bool odd = false;
 #pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                float4 q = {-kInf, -kInf, -kInf, -kInf};
-                if (e0 + j < E)
-                    q = *reinterpret_cast<const float4 *>(row + e0 + j);
-                l[j] = q.x;
-                l[j + 1] = q.y;
-                l[j + 2] = q.z;
-                l[j + 3] = q.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                l[j] = e0 + j < E ? row[e0 + j] : -kInf;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            l[j] = e0 + j < E ? row[e0 + j] : -kInf;
+    for (int j = 0; j < N; j += 4) {
+        const float4 q = load4<float4, float>(row, live ? expert(j) : E, E, wide, -kInf);
+        l[j] = q.x;
+        l[j + 1] = q.y;
+        l[j + 2] = q.z;
+        l[j + 3] = q.w;
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (!(l[j] < kInf)) {
-            bad = true;
-            l[j] = -kInf;
-        }
-        l[j] += 0.0f;  // -0 orders as 0
+    for (int j = 0; j < N; ++j)
+        odd |= !(l[j] < kInf);
+    if (__ballot(odd)) {
+        bad |= odd;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            l[j] = l[j] < kInf ? l[j] : -kInf;
     }
 }
 
-__device__ __forceinline__ float wave_max_float(float v) { return unordered(wave_max(ordered(v))); }
+template <int N>
+__device__ __forceinline__ float largest(const float (&l)[N])
+{
+    float m = l[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j)
+        m = fmaxf(m, l[j]);
+    return row_max(m);
+}
 
 // Unnormalised scores with a common factor that keeps the largest near one:
 // softmax exp(l - ref), ref the largest logit; sigmoid s / exp(ref), ref the
@@ -76,340 +99,617 @@ __device__ __forceinline__ float raw_score(float l, float ref)
 }
 
 template <bool SIGMOID>
-__device__ __forceinline__ float score_ref(float largest)
+__device__ __forceinline__ float score_ref(float top)
 {
-    return SIGMOID ? fminf(largest, 0.0f) : largest;
+    return SIGMOID ? fminf(top, 0.0f) : top;
 }
 
-template <int V, bool SIGMOID>
-__device__ __forceinline__ float raw_scores(const float (&l)[V], float (&s)[V])
+// A token's shares p of one, and with `slopes` the factor of their gradient
+// (softmax 1; sigmoid 1 - s). An expert that is not live has p = 0.
+template <int N, bool SIGMOID>
+__device__ __forceinline__ void shares_of(const float (&l)[N], float (&p)[N], float *slopes)
 {
-    float m = l[0];
+    float top = 0.0f, sum = 0.0f;
+    if constexpr (SIGMOID) {
 #pragma unroll
-    for (int j = 1; j < V; ++j)
-        m = fmaxf(m, l[j]);
-    m = score_ref<SIGMOID>(wave_max_float(m));
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        s[j] = raw_score<SIGMOID>(l[j], m);
-        sum += s[j];
-    }
-    return wave_sum(sum);
-}
-
-// The two largest of a group's keys, by lanes that each look at every P-th of
-// the group's experts; -inf keys do not count. Every lane of group g (lanes
-// g P .. g P + P - 1) gets the sum; -inf for a group without experts.
-template <typename F>
-__device__ __forceinline__ F group_score(const F *key, int g, int size, int P, int G)
-{
-    F a = (F)-kInf, b = (F)-kInf;
-    if (g < G)
-        for (int i = lane_id() % P; i < size; i += P) {
-            const F k = key[g * size + i];
-            b = k > a ? a : k > b ? k : b;
-            a = k > a ? k : a;
+        for (int j = 0; j < N; ++j) {
+            const float t = exp_fp32(-fabsf(l[j]));  // 0 for -inf
+            const float r = __builtin_amdgcn_rcpf(1.0f + t), u = t * r;
+            p[j] = l[j] >= 0.0f ? r : u;
+            if (slopes)
+                slopes[j] = l[j] >= 0.0f ? u : r;
+            sum += p[j];
         }
-    for (int d = 1; d < P; d <<= 1) {
-        const F oa = __shfl_xor(a, d, kWave), ob = __shfl_xor(b, d, kWave);
-        b = oa > a ? (a > ob ? a : ob) : (oa > b ? oa : b);
-        a = oa > a ? oa : a;
+        sum = row_sum(sum);
+        // scores that are all near their underflow, relative to the largest
+        if (__ballot(sum < 0x1p-60f)) {
+            top = largest(l);
+            sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                p[j] = raw_score<true>(l[j], score_ref<true>(top));
+                sum += p[j];
+            }
+            sum = row_sum(sum);
+        }
+    } else {
+        top = largest(l);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            p[j] = exp_fp32(l[j] - top);  // 0 for -inf (and -inf less itself, a NaN)
+            sum += p[j];
+        }
+        sum = row_sum(sum);
     }
-    return b > (F)-kInf ? a + b : a;
+    const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        p[j] *= r;
 }
 
-// Bit g of the result: group g is one of the `top` best (ties to the lower
-// group). near: a kept and a dropped group's scores lie within tol of each
-// other. 64 / P >= G; score is the same in the P lanes of a group.
-template <typename F>
-__device__ __forceinline__ uint64_t best_groups(F score, int P, int G, int top, F tol, bool &near)
+// ------------------------------------------------------------------- choice
+//
+// The choice is that of the exact scores. It is made on whole numbers that
+// rise with the keys (score + bias; without a bias the logits themselves): a
+// key's distance from the token's largest in fixed point, with the expert's
+// number below it, so that one unsigned maximum or minimum moves both and
+// equal keys order by their experts. Each lane sorts its experts in such
+// words, lists of the L best are merged over the 16 lanes, and a token whose
+// outcome falls between keys that are nearer than their error (or than the
+// fixed point tells), unless these are of equal logits and biases, is done
+// again in 64 bits.
+
+// Fixed point: B bits for a window below the token's largest key. Keys below
+// the window all have 0, as does what is not live (and what the conversion
+// gets as a NaN or less than nothing): a token that takes such a key is done
+// again.
+template <int N>
+struct Word {
+    static constexpr int kId = N == 4 ? 6 : N == 8 ? 7 : N == 16 ? 8 : 9;
+    static constexpr uint32_t kIdMask = (1u << kId) - 1u;
+    static constexpr int kBits = N <= 16 ? 24 : 23;  // what fp32 counts exactly
+    static constexpr float kMost = (float)((1u << kBits) - 1u);
+    static __device__ __forceinline__ uint32_t make(float key, float top, float per_unit, int e)
+    {
+        uint32_t f;  // as the instruction does: 0 below nothing and for a NaN
+        asm("v_cvt_u32_f32 %0, %1" : "=v"(f) : "v"(__builtin_fmaf(key - top, per_unit, kMost)));
+        return (f << kId) | (kIdMask - (uint32_t)e);
+    }
+    static __device__ __forceinline__ int id(uint32_t w) { return (int)(kIdMask - (w & kIdMask)); }
+    static __device__ __forceinline__ int key(uint32_t w) { return (int)(w >> kId); }
+};
+
+// Width of the window: logits, and keys that are scores with a bias.
+constexpr float kLogitWindow = 32.0f, kKeyWindow = 2.0f;
+
+__device__ __forceinline__ void descend(uint32_t &a, uint32_t &b)
 {
-    const int g = lane_id() / P;
-    int rank = 0;
-    for (int o = 0; o < G; ++o) {
-        const F s = __shfl(score, o * P, kWave);
-        rank += s > score || (s == score && o < g);
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+
+// Any order -> descending.
+template <int M>
+__device__ __forceinline__ void sort_words(uint32_t (&w)[M])
+{
+#pragma unroll
+    for (int k = 2; k <= M; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j > 0; j /= 2)
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                const int o = i ^ j;
+                if (o > i) {
+                    if ((i & k) == 0)
+                        descend(w[i], w[o]);
+                    else
+                        descend(w[o], w[i]);
+                }
+            }
+}
+
+// One that falls and then rises (or the reverse) -> descending.
+template <int M>
+__device__ __forceinline__ void sort_bitonic(uint32_t (&w)[M])
+{
+#pragma unroll
+    for (int j = M / 2; j > 0; j /= 2)
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            if ((i ^ j) > i)
+                descend(w[i], w[i ^ j]);
+}
+
+// The L best of a lane's N words, descending.
+template <int N, int L>
+__device__ __forceinline__ void best_of_lane(const uint32_t (&w)[N], uint32_t (&best)[L])
+{
+    if constexpr (N <= L) {
+        uint32_t s[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            s[j] = w[j];
+        sort_words<N>(s);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            best[j] = j < N ? s[j < N ? j : 0] : 0u;
+    } else {
+#pragma unroll
+        for (int p = 0; p < N; p += L) {
+            uint32_t s[L];
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                s[j] = w[p + j];
+            sort_words<L>(s);
+            if (p == 0) {
+#pragma unroll
+                for (int j = 0; j < L; ++j)
+                    best[j] = s[j];
+            } else {
+                // of two descending lists the larger of i-th and (L-1-i)-th
+                // are the L best
+#pragma unroll
+                for (int j = 0; j < L; ++j)
+                    best[j] = max(best[j], s[L - 1 - j]);
+                sort_bitonic<L>(best);
+            }
+        }
     }
-    const bool kept = g < G && rank < top && score > (F)-kInf;
-    uint64_t bits = 0, todo = uniform64(__ballot(kept && lane_id() % P == 0));
-    while (todo) {
-        bits |= 1ull << (__builtin_ctzll(todo) / P);
-        todo &= todo - 1;
+}
+
+template <int L, int CTRL>
+__device__ __forceinline__ void merge_lanes(uint32_t (&best)[L])
+{
+    uint32_t o[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+        o[j] = (uint32_t)EPX_DPP(best[j], 0, CTRL, 0xF);
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+        best[j] = max(best[j], o[L - 1 - j]);
+    sort_bitonic<L>(best);
+}
+
+// How near two keys may be and yet stand the other way round when exact: twice
+// a key's error. Without a bias the words rise with the logits themselves and
+// only equal ones tell nothing. With one, a key is off by
+//   the sigmoid's error, below 3e-7: its exponential is within
+//     (1.25 |l| + 2) 2^-24 of itself, which s (1 - s) |l| < 0.224 and s (1 - s)
+//     <= 1/4 scale down, then an addition's rounding and a reciprocal's unit;
+//   the softmax's, below 4e-6 of the token's largest score for a pair (the sum
+//     of 512 terms, each within (2.25 |x| + 2) 2^-24, is common to both);
+//   the bias's addition, 2^-24 of the key.
+template <bool SIGMOID>
+__device__ __forceinline__ float pair_tol(float largest_score, float largest_key)
+{
+    return (SIGMOID ? 0x1p-20f : 0x1p-17f * largest_score) + 0x1p-22f * largest_key;
+}
+
+// LDS of a wave's four tokens.
+template <int N, int L>
+struct RouteLds {
+    // a unit of a group is one expert's key, or where groups are made of fours
+    // the two best of these; spread so that lanes which walk different groups
+    // meet different banks
+    float unit[kTokens][kRow * N + kRow * N / 8 + 4];
+    float score[kTokens][64];
+    uint32_t chosen[kTokens][L];
+    double key64[kRow * N];
+    uint16_t candidate[kRow * N];
+    static __device__ __forceinline__ int at(int u) { return u + (u >> 3); }
+};
+
+// What a wave wrote to LDS is there for its other lanes.
+__device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// Bits of the groups that stay, at (group * P); near: a kept and a dropped
+// group's scores are within tol of each other. P lanes of a token walk a group
+// of `units` units (P = 1 with more than 16 groups, when a lane has several).
+template <int N, int L>
+__device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, RouteLds<N, L> &lds, int P,
+                                                int units, bool fours, float tol, bool &near)
+{
+    const int row = lane_id() / kRow, i = row_lane();
+    const float *unit = lds.unit[row];
+    float *score = lds.score[row];
+    for (int g = i / P; g < a.G; g += kRow / P) {
+        float x = -kInf, y = -kInf;
+#pragma unroll 4
+        for (int m = i % P; m < units; m += P) {
+            const int u = RouteLds<N, L>::at(g * units + m);
+            const float k = unit[fours ? 2 * u : u];
+            y = fmaxf(y, fminf(x, k));
+            x = fmaxf(x, k);
+            if (fours)
+                y = fmaxf(y, unit[2 * u + 1]);
+        }
+        for (int d = 1; d < P; d <<= 1) {
+            const float ox = __shfl_xor(x, d, kWave), oy = __shfl_xor(y, d, kWave);
+            y = fmaxf(fmaxf(y, oy), fminf(x, ox));
+            x = fmaxf(x, ox);
+        }
+        if (i % P == 0)
+            score[g] = y > -kInf ? x + y : x;
     }
-    // the least kept and the best dropped score
-    F lo = kept ? score : (F)kInf, hi = kept || g >= G ? (F)-kInf : score;
-    for (int d = 1; d < kWave; d <<= 1) {
-        const F ol = __shfl_xor(lo, d, kWave), oh = __shfl_xor(hi, d, kWave);
-        lo = ol < lo ? ol : lo;
-        hi = oh > hi ? oh : hi;
+    wave_lds();
+    uint64_t bits = 0;
+    float lo = kInf, hi = -kInf;
+    for (int g0 = 0; g0 < a.G; g0 += kRow / P) {
+        const int g = g0 + i / P;
+        const float mine = g < a.G ? score[g] : -kInf;
+        int rank = 0;
+#pragma unroll 4
+        for (int o = 0; o < a.G; ++o) {
+            const float s = score[o];
+            rank += s > mine || (s == mine && o < g);
+        }
+        const bool kept = g < a.G && rank < a.top_groups && mine > -kInf;
+        bits |= (uint64_t)row_ballot(kept && i % P == 0) << (g0 * P);
+        lo = kept ? fminf(lo, mine) : lo;
+        hi = kept ? hi : fmaxf(hi, mine);
     }
-    near = lo < (F)kInf && hi > (F)-kInf && lo - hi <= tol;
+    lo = -row_max(-lo);
+    hi = row_max(hi);
+    near = lo < kInf && hi > -kInf && lo - hi <= tol;
     return bits;
 }
 
-// The choice in 64 bits, one expert a round: lane r of the result has the
-// r-th expert, or -1.
-template <int V, bool SIGMOID>
-__device__ __noinline__ int choose64(const RouteArgs &a, const float (&l)[V], double *lds, int P)
-{
-    const int lane = lane_id(), e0 = lane * V;
-    double key[V];
-    if constexpr (SIGMOID) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            key[j] = l[j] > -kInf ? 1.0 / (1.0 + exp(-(double)l[j])) : -(double)kInf;
-    } else {
-        float m = l[0];
-#pragma unroll
-        for (int j = 1; j < V; ++j)
-            m = fmaxf(m, l[j]);
-        const double ref = (double)wave_max_float(m);
-        double sum = 0.0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            key[j] = l[j] > -kInf ? exp((double)l[j] - ref) : 0.0;
-            sum += key[j];
-        }
-        for (int d = 1; d < kWave; d <<= 1)
-            sum += __shfl_xor(sum, d, kWave);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            key[j] = l[j] > -kInf ? key[j] / sum : -(double)kInf;
-    }
-    double order[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (a.bias && e0 + j < a.E) {
-            const float b = a.bias[e0 + j];
-            key[j] = b < kInf ? key[j] + (double)b : -(double)kInf;
-        }
-        // without a bias the logits are in the scores' order
-        order[j] = a.bias ? key[j] : (double)l[j];
-    }
-    if (a.G > 1) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j < a.E)
-                lds[e0 + j] = key[j];
-        __builtin_amdgcn_wave_barrier();
-        const double s = group_score<double>(lds, lane / P, a.group_size, P, a.G);
-        bool near;
-        const uint64_t kept = best_groups<double>(s, P, a.G, a.top_groups, 0.0, near);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j < a.E && !(kept >> div_by_magic(e0 + j, a.size_mul) & 1))
-                order[j] = -(double)kInf;
-    }
-    int mine = -1;
-    for (int r = 0; r < a.K; ++r) {
-        double best = order[0];
-        int e = e0;
-#pragma unroll
-        for (int j = 1; j < V; ++j)
-            if (order[j] > best) {
-                best = order[j];
-                e = e0 + j;
-            }
-        for (int d = 1; d < kWave; d <<= 1) {
-            const double ob = __shfl_xor(best, d, kWave);
-            const int oe = __shfl_xor(e, d, kWave);
-            if (ob > best || (ob == best && oe < e)) {
-                best = ob;
-                e = oe;
-            }
-        }
-        if (!(best > -(double)kInf))
-            break;
-        if (lane == r)
-            mine = e;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j == e)
-                order[j] = -(double)kInf;
-    }
-    return mine;
-}
-
-constexpr int kTokens = 4;  // tokens (waves) of a block
-
-// How far an fp32 key k may be from the exact one, for both of a pair: twice
-// the error of the score -- sigmoid below 3e-7 (exp within 2^-22 of itself
-// wherever s (1 - s) |l| matters), softmax below 2.3e-6 (the same, and the
-// rounding of a sum over 512 experts) -- and of the bias's addition, 2^-24 of
-// the key.
+// Scores in 64 bits, one token's by the whole wave.
 template <bool SIGMOID>
-__device__ __forceinline__ float key_tol(float k)
+struct Exact {
+    const RouteArgs &a;
+    const float *row;
+    double top, sum;
+    __device__ __forceinline__ Exact(const RouteArgs &args, int64_t t)
+        : a(args), row(args.logits + (size_t)t * args.E), top(0.0), sum(0.0)
+    {
+        if constexpr (!SIGMOID) {
+            float m = -kInf;
+            for (int e = lane_id(); e < a.E; e += kWave)
+                m = fmaxf(m, logit(e));
+            for (int d = 1; d < kWave; d <<= 1)
+                m = fmaxf(m, __shfl_xor(m, d, kWave));
+            top = (double)m;
+            for (int e = lane_id(); e < a.E; e += kWave) {
+                const float l = logit(e);
+                sum += l > -kInf ? exp((double)l - top) : 0.0;
+            }
+            for (int d = 1; d < kWave; d <<= 1)
+                sum += __shfl_xor(sum, d, kWave);
+        }
+    }
+    __device__ __forceinline__ float logit(int e) const { return row[e] < kInf ? row[e] : -kInf; }
+    // score and bias, -inf if the expert can not be chosen
+    __device__ __forceinline__ double key(int e) const
+    {
+        const double l = (double)logit(e);
+        if (!(l > -(double)kInf))
+            return l;
+        const double s = SIGMOID ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
+        if (!a.bias)
+            return s;
+        const float b = a.bias[e];
+        return b < kInf ? s + (double)b : -(double)kInf;
+    }
+};
+
+// One token's groups in 64 bits by the whole wave: bit g for a group that stays.
+template <int N, int L, bool SIGMOID>
+__device__ __noinline__ uint64_t groups64(const RouteArgs &a, int64_t t, RouteLds<N, L> &lds)
 {
-    return (SIGMOID ? 0x1p-20f : 0x1p-17f) * (1.0f + fabsf(k));
+    const Exact<SIGMOID> exact(a, t);
+    const int lane = lane_id();
+    for (int e = lane; e < a.E; e += kWave)
+        lds.key64[e] = exact.key(e);
+    wave_lds();
+    int P = 1;  // lanes of a group
+    while (2 * P * a.G <= kWave)
+        P *= 2;
+    const int g = lane / P;
+    double x = -(double)kInf, y = x;
+    if (g < a.G)
+        for (int m = lane % P; m < a.group_size; m += P) {
+            const double k = lds.key64[g * a.group_size + m];
+            y = k > x ? x : k > y ? k : y;
+            x = k > x ? k : x;
+        }
+    for (int d = 1; d < P; d <<= 1) {
+        const double ox = __shfl_xor(x, d, kWave), oy = __shfl_xor(y, d, kWave);
+        y = ox > x ? (x > oy ? x : oy) : (ox > y ? ox : y);
+        x = ox > x ? ox : x;
+    }
+    const double mine = y > -(double)kInf ? x + y : x;
+    int rank = 0;
+    for (int o = 0; o < a.G; ++o) {
+        const double s = __shfl(mine, o * P, kWave);
+        rank += s > mine || (s == mine && o < g);
+    }
+    uint64_t todo = uniform64(__ballot(g < a.G && lane % P == 0 && rank < a.top_groups &&
+                                       mine > -(double)kInf));
+    uint64_t bits = 0;
+    for (; todo; todo &= todo - 1)
+        bits |= 1ull << (__builtin_ctzll(todo) / P);
+    return bits;
 }
 
-template <int V, bool SIGMOID, bool NORM>
-__global__ __launch_bounds__(kWave *kTokens) void route_kernel(RouteArgs a, bool wide, int P)
+// One token's choice in 64 bits by the whole wave, among n candidates: chosen[r]
+// is the r-th expert's number, or ~0.
+template <int N, int L, bool SIGMOID>
+__device__ __noinline__ void choose64(const RouteArgs &a, int64_t t, int n, RouteLds<N, L> &lds,
+                                      uint32_t *chosen)
 {
-    __shared__ double lds_all[kTokens][V * kWave];
-    __shared__ float key_all[kTokens][V * kWave];
-    const int wave = threadIdx.x >> 6, lane = lane_id(), e0 = lane * V;
-    const int64_t t = (int64_t)blockIdx.x * kTokens + wave;
-    if (t >= a.T)
-        return;
-    double *lds = lds_all[wave];
-    if (a.mask && !a.mask[t]) {
-        if (lane < a.K) {
-            a.topk_idx[t * a.K + lane] = -1;
-            a.topk_w[t * a.K + lane] = 0.0f;
-        }
-        return;
+    const int lane = lane_id();
+    if (a.bias) {
+        const Exact<SIGMOID> exact(a, t);
+        for (int c = lane; c < n; c += kWave)
+            lds.key64[c] = exact.key(lds.candidate[c]);
+    } else {  // the logits order
+        for (int c = lane; c < n; c += kWave)
+            lds.key64[c] = (double)a.logits[(size_t)t * a.E + lds.candidate[c]];
     }
-    float l[V];
+    if (lane < L)
+        chosen[lane] = ~0u;
+    wave_lds();
+    for (int c = lane; c < n; c += kWave) {
+        const int e = lds.candidate[c];
+        const double k = lds.key64[c];
+        int rank = 0;
+#pragma unroll 4
+        for (int o = 0; o < n; ++o) {
+            const double ok = lds.key64[o];
+            rank += ok > k || (ok == k && lds.candidate[o] < e);
+        }
+        if (rank < a.K)
+            chosen[rank] = (uint32_t)e;
+    }
+    wave_lds();
+}
+
+template <int N, int L, bool SIGMOID>
+__global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bool wide_bias,
+                                                      int P, bool normalize)
+{
+    typedef Word<N> W;
+    __shared__ RouteLds<N, L> lds;
+    const int row = lane_id() / kRow, i = row_lane();
+    const int64_t t = (int64_t)blockIdx.x * kTokens + row;
+    const bool live = t < a.T && (!a.mask || a.mask[t]);
+    const float *logits = a.logits + (size_t)t * a.E;
+    float l[N];
     bool bad = false;
-    load_logits<V>(a.logits + (size_t)t * a.E, a.E, wide, l, bad);
-    // scores are needed whole by a bias, by groups and by weights that are
-    // not normalised
-    float s[V], sum = 1.0f;
-    const bool scored = a.bias || a.G > 1 || (!NORM && !SIGMOID);
-    if (scored) {
+    load_logits<N>(logits, a.E, wide, live, l, bad);
+    const float top_l = largest(l);
+
+    // order values: the logits, or scores with their bias
+    float order[N];
+    float per_unit = (W::kMost + 1.0f) / kLogitWindow, top = top_l;
+    int tol = 0;
+    bool near = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        order[j] = l[j];
+    if (a.bias || a.G > 1) {
+        float best = 0.0f, key[N], most = 0.0f;  // most: largest magnitude of a key
         if constexpr (SIGMOID) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                s[j] = raw_score<true>(l[j], 0.0f);
+            for (int j = 0; j < N; ++j)
+                key[j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[j] * -0x1.715476p+0f));
+            most = 1.0f;
         } else {
-            sum = raw_scores<V, false>(l, s);
+            float sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                s[j] /= sum;
+            for (int j = 0; j < N; ++j) {
+                key[j] = __builtin_amdgcn_exp2f((l[j] - top_l) * 0x1.715476p+0f);
+                sum += l[j] > -kInf ? key[j] : 0.0f;
+            }
+            best = most = __builtin_amdgcn_rcpf(row_sum(sum));  // of the largest logit
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                key[j] *= best;
+        }
+        if (a.bias) {
+            bool odd = false;
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                const float4 q = load4<float4, float>(a.bias, expert(j), a.E, wide_bias, 0.0f);
+                const float b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    key[j + r] += b[r];
+                    odd |= !(fabsf(b[r]) < kInf);
+                    m = fmaxf(m, fabsf(b[r]));
+                }
+            }
+            if (__ballot(odd)) {  // -inf: not chosen; NaN, +inf: nor those
+                m = 0.0f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float b = expert(j) < a.E ? a.bias[expert(j)] : 0.0f;
+                    const bool can = fabsf(b) < kInf;
+                    bad |= live && !(b < kInf);
+                    key[j] = can ? key[j] : -kInf;
+                    m = fmaxf(m, can ? fabsf(b) : 0.0f);
+                }
+            }
+            most += row_max(m);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            key[j] = l[j] > -kInf ? key[j] : -kInf;
+        const float pair = pair_tol<SIGMOID>(best, most);
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                order[j] = key[j];
+        }
+        if (a.G > 1) {
+            const bool fours = a.group_size % 4 == 0;
+            float *unit = lds.unit[row];
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                if (fours) {
+                    const float x = fmaxf(key[j], key[j + 1]), u = fminf(key[j], key[j + 1]);
+                    const float y = fmaxf(key[j + 2], key[j + 3]), v = fminf(key[j + 2], key[j + 3]);
+                    const int at = 2 * RouteLds<N, L>::at(expert(j) >> 2);
+                    unit[at] = fmaxf(x, y);
+                    unit[at + 1] = fmaxf(fmaxf(u, v), fminf(x, y));
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        unit[RouteLds<N, L>::at(expert(j) + r)] = key[j + r];
+                }
+            }
+            wave_lds();
+            // a score is two keys and a rounding
+            uint64_t kept = best_groups<N, L>(
+                a, lds, P, fours ? a.group_size >> 2 : a.group_size, fours, 3.0f * pair, near);
+            const uint64_t unsure = uniform64(__ballot(near && live));
+            for (int q = 0; unsure && q < kTokens; ++q) {
+                if (!(unsure >> (q * kRow) & 0xFFFF))
+                    continue;
+                uint64_t bits = groups64<N, L, SIGMOID>(
+                    a, (int64_t)blockIdx.x * kTokens + q, lds);
+                if (row == q) {
+                    kept = 0;
+                    for (; bits; bits &= bits - 1)
+                        kept |= 1ull << (P * __builtin_ctzll(bits));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int g = div_by_magic(expert(j) + (fours ? 0 : r), a.size_mul);
+                    const bool stays = kept >> (P * g & 63) & 1;
+                    order[j + r] = stays && key[j + r] > -kInf ? order[j + r] : -kInf;
+                }
+            }
+        }
+        top = largest(order);
+        if (a.bias) {
+            per_unit = (W::kMost + 1.0f) / kKeyWindow;
+            tol = (int)fminf(pair * per_unit, W::kMost) + 2;
         }
     }
-    float order[V];
+    uint32_t w[N], best[L];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        order[j] = l[j];
-    if (a.bias) {
+    for (int j = 0; j < N; ++j)
+        w[j] = W::make(order[j], top, per_unit, expert(j));
+    best_of_lane<N, L>(w, best);
+    merge_lanes<L, 0x128>(best);  // row_ror: 8, 4, 2, 1
+    merge_lanes<L, 0x124>(best);
+    merge_lanes<L, 0x122>(best);
+    merge_lanes<L, 0x121>(best);
+    if (i == 0) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            if (e0 + j < a.E) {
-                const float b = a.bias[e0 + j];
-                if (!(b < kInf))
-                    bad = true;
-                order[j] = l[j] > -kInf && b < kInf ? s[j] + b : -kInf;
+        for (int j = 0; j < L; ++j)
+            lds.chosen[row][j] = best[j];
+    }
+    wave_lds();
+    // the K-th, and whether one that is left out is as near
+    const uint32_t last = lds.chosen[row][a.K - 1];
+    const uint32_t from = W::key(last) > tol ? (uint32_t)(W::key(last) - tol) << W::kId : 0u;
+    bool beside = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        beside |= w[j] - from < last - from;
+    // (all experts again where the K-th is below the window or not live)
+    const bool blind = live && W::key(last) <= tol;
+    near = blind;
+    if (__ballot(beside && live && !blind)) {
+        const int le = W::id(last);
+        const bool look = beside && live && !blind;
+        const float ll = look ? logits[le] : 0.0f;
+        const float lb = look && a.bias ? a.bias[le] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (look && w[j] - from < last - from)
+                near |= l[j] != ll || (a.bias && a.bias[expert(j)] != lb);
+    }
+    constexpr int kPer = (L + kRow - 1) / kRow;  // entries of a lane: i, i + 16
+    int e[kPer];
+    float lk[kPer];
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+        const int r = i + m * kRow;
+        const bool have = live && !blind && r < a.K;
+        const uint32_t mine = have ? lds.chosen[row][r] : 0u;
+        e[m] = have ? W::id(mine) : -1;
+        lk[m] = have ? logits[e[m]] : -kInf;
+        const uint32_t next = have && r + 1 < a.K ? lds.chosen[row][r + 1] : 0u;
+        if (next && W::key(mine) - W::key(next) <= tol) {
+            const int ne = W::id(next);
+            near |= lk[m] != logits[ne] || (a.bias && a.bias[e[m]] != a.bias[ne]);
+        }
+    }
+    const uint64_t again = uniform64(__ballot(near));
+    if (again) {
+        for (int q = 0; q < kTokens; ++q) {
+            if (!(again >> (q * kRow) & 0xFFFF))
+                continue;
+            // the experts that are not clearly below the K-th
+            int n = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const bool can = row == q && order[j] > -kInf && (blind || w[j] >= from);
+                const uint64_t m = uniform64(__ballot(can));
+                if (can)
+                    lds.candidate[n + __builtin_popcountll(m & lanes_below(lane_id()))] =
+                        (uint16_t)expert(j);
+                n += __builtin_popcountll(m);
+            }
+            wave_lds();
+            choose64<N, L, SIGMOID>(a, (int64_t)blockIdx.x * kTokens + q, n, lds, lds.chosen[q]);
+        }
+        if (again >> (row * kRow) & 0xFFFF) {
+#pragma unroll
+            for (int m = 0; m < kPer; ++m) {
+                const int r = i + m * kRow;
+                e[m] = r < a.K ? (int)lds.chosen[row][r] : -1;
+                lk[m] = e[m] >= 0 ? logits[e[m]] : -kInf;
             }
         }
     }
-    if (__ballot(bad) && lane == 0)
-        flag_error(a.err, EPX_DEV_BAD_LOGIT);
-    bool near = false;
-    if (a.G > 1) {
-        float *key = key_all[wave];
-        float top = 0.0f;
+    // weights
+    float v[kPer], total = 1.0f;
+    if (normalize) {
+        float m = lk[0], sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j < a.E) {
-                const float k = a.bias ? order[j] : l[j] > -kInf ? s[j] : -kInf;
-                key[e0 + j] = k;
-                top = fmaxf(top, k > -kInf ? fabsf(k) : 0.0f);
-            }
-        __builtin_amdgcn_wave_barrier();
-        const float score = group_score<float>(key, lane / P, a.group_size, P, a.G);
-        // a score is two keys, and rounded once more
-        const float tol = 2.5f * key_tol<SIGMOID>(wave_max_float(top));
-        const uint64_t kept = best_groups<float>(score, P, a.G, a.top_groups, tol, near);
+        for (int q = 1; q < kPer; ++q)
+            m = fmaxf(m, lk[q]);
+        const float ref = score_ref<SIGMOID>(row_max(m));
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j < a.E && !(kept >> div_by_magic(e0 + j, a.size_mul) & 1))
-                order[j] = -kInf;
-    }
-    // each lane's experts in descending order (neighbours exchanged only where
-    // strictly out of order, so equal values keep the experts' order)
-    uint32_t k[V];
-    int id[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        k[j] = order[j] > -kInf ? ordered(order[j]) : 0u;
-        id[j] = e0 + j;
-    }
-#pragma unroll
-    for (int p = 0; p < V; ++p)
-#pragma unroll
-        for (int j = p & 1; j + 1 < V; j += 2) {
-            const bool swap = k[j + 1] > k[j];
-            const uint32_t ka = swap ? k[j + 1] : k[j], kb = swap ? k[j] : k[j + 1];
-            const int ia = swap ? id[j + 1] : id[j], ib = swap ? id[j] : id[j + 1];
-            k[j] = ka; k[j + 1] = kb;
-            id[j] = ia; id[j + 1] = ib;
+        for (int q = 0; q < kPer; ++q) {
+            v[q] = raw_score<SIGMOID>(lk[q], ref);
+            sum += v[q];
         }
-    // one expert a round, the best of the lanes' firsts; lane r keeps the r-th
-    // (and, to see how near the first one left out is, the K-th)
-    int mine = -1;
-    uint32_t mine_key = 0;
-    const int rounds = a.bias ? a.K + 1 : a.K;
-    for (int r = 0; r < rounds; ++r) {
-        const uint32_t best = wave_max(k[0]);
-        if (best == 0)
-            break;
-        const int from = __builtin_ctzll(__ballot(k[0] == best));
-        const int e = __builtin_amdgcn_readlane(id[0], from);
-        if (lane == r) {
-            mine = e;
-            mine_key = best;
-        }
-        if (lane == from) {
-#pragma unroll
-            for (int j = 0; j + 1 < V; ++j) {
-                k[j] = k[j + 1];
-                id[j] = id[j + 1];
-            }
-            k[V - 1] = 0;
-        }
-    }
-    // the chosen logits (lane e / V holds expert e)
-    const auto pick = [&](int e) {
-        float v = -kInf;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float o = __shfl(l[j], e / V, kWave);
-            if (e % V == j)
-                v = o;
-        }
-        return v;
-    };
-    float lk = pick(mine < 0 ? 0 : mine);
-    if (a.bias) {
-        // a neighbour in the order that is nearer than the keys' errors,
-        // unless the two are alike in logit and bias
-        const int oe = __shfl_down(mine, 1, kWave);
-        const float ok = unordered((uint32_t)__shfl_down((int)mine_key, 1, kWave));
-        const float ol = __shfl_down(lk, 1, kWave);
-        if (lane < a.K && mine >= 0 && oe >= 0) {
-            const float mk = unordered(mine_key);
-            near |= mk - ok <= key_tol<SIGMOID>(mk) &&
-                    !(lk == ol && a.bias[mine] == a.bias[oe]);
-        }
-    }
-    if (__ballot(near)) {
-        mine = choose64<V, SIGMOID>(a, l, lds, P);
-        lk = pick(mine < 0 ? 0 : mine);
-    }
-    const bool have = lane < a.K && mine >= 0;
-    lk = have ? lk : -kInf;
-    float w;
-    if constexpr (NORM) {
-        const float ref = score_ref<SIGMOID>(wave_max_float(lk));
-        const float n = raw_score<SIGMOID>(lk, ref);
-        const float total = wave_sum(n);
-        w = n / total;
+        total = row_sum(sum);
     } else if constexpr (SIGMOID) {
-        w = raw_score<true>(lk, 0.0f);
-    } else {
-        float m = l[0];
 #pragma unroll
-        for (int j = 1; j < V; ++j)
-            m = fmaxf(m, l[j]);
-        w = raw_score<false>(lk, wave_max_float(m)) / sum;
+        for (int q = 0; q < kPer; ++q)
+            v[q] = raw_score<true>(lk[q], 0.0f);
+    } else {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            sum += exp_fp32(l[j] - top_l);  // 0 for -inf
+        total = row_sum(sum);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+            v[q] = raw_score<false>(lk[q], top_l);
     }
-    if (lane < a.K) {
-        a.topk_idx[t * a.K + lane] = have ? mine : -1;
-        a.topk_w[t * a.K + lane] = have ? a.scale * w : 0.0f;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int r = i + q * kRow;
+        if (t < a.T && r < a.K) {
+            a.topk_idx[t * a.K + r] = e[q];
+            a.topk_w[t * a.K + r] = e[q] >= 0 ? a.scale * (v[q] / total) : 0.0f;
+        }
     }
+    if (bad)
+        flag_error(a.err, EPX_DEV_BAD_LOGIT);
 }
 
 // -------------------------------------------------------------- balance loss
@@ -419,19 +719,30 @@ __global__ __launch_bounds__(kWave *kTokens) void route_kernel(RouteArgs a, bool
 //   loss_s = E / (K n) sum_e c_e P_e,  loss = mean of loss_s over the
 // sequences with n > 0 (0 without any).
 //
-// First launch: a block has a run of tokens and leaves one row of sums per
-// sequence that meets the run, at row (run + sequence), which is a place of
-// its own because the runs' and sequences' numbers ascend together. Second
-// launch: a block per sequence adds its rows in order; the last block to end
-// adds the losses. A batch of one run needs the first launch alone.
+// First launch: a block has a run of consecutive tokens, one for each 16
+// lanes, and leaves a row of sums for each sequence that meets the run, at row
+// (run + sequence): a place of its own, because runs and sequences ascend
+// together. Second launch: a block has 64 experts of one sequence and adds
+// their rows; the last block to end adds the losses. A batch of one run needs
+// the first launch alone.
 
-constexpr int kRun = 64;       // tokens of a run
-constexpr int kRunWaves = 16;  // waves that share it
-constexpr int kFinalThreads = 1024;
+template <int N>
+struct Run {
+    static constexpr int kTokensOfRun = N == 32 ? 32 : 64;
+    static constexpr int kWaves = kTokensOfRun / kTokens;
+    static constexpr int kColumns = kRow * N;
+    static constexpr int kThreads = kWaves * kWave;
+    // threads of a column share the run's tokens
+    static constexpr int kShares = kThreads / kColumns < kTokensOfRun ? kThreads / kColumns
+                                                                      : kTokensOfRun;
+    static constexpr int kShare = kTokensOfRun / kShares;
+};
+
+constexpr int kFinalColumns = 64, kFinalThreads = 256;
 
 struct BalanceWs {
     unsigned int *done;  // blocks of the second launch that have ended
-    float *seq_loss;     // [S]
+    float *dot;          // [S, ceil(E / 64)]: sums of counts * probs
     int *seen;           // [rows]
     int *counts;         // [rows, E]
     float *probs;        // [rows, E]
@@ -439,20 +750,23 @@ struct BalanceWs {
 
 __host__ __device__ inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-__host__ __device__ inline int64_t balance_rows(int T, int S)
+__host__ __device__ inline int run_tokens(int E) { return E > 256 ? 32 : 64; }
+
+__host__ __device__ inline int64_t balance_rows(int T, int E, int S)
 {
-    return (T + kRun - 1) / kRun + (int64_t)S;
+    return ((int64_t)T + run_tokens(E) - 1) / run_tokens(E) + (int64_t)S;
 }
 
 __host__ __device__ inline BalanceWs balance_ws(void *ws, int T, int E, int S)
 {
-    const int64_t rows = balance_rows(T, S);
+    const int64_t rows = balance_rows(T, E, S);
+    const size_t parts = (E + kFinalColumns - 1) / kFinalColumns;
     char *p = static_cast<char *>(ws);
     BalanceWs w;
     w.done = reinterpret_cast<unsigned int *>(p);
     p += 16;
-    w.seq_loss = reinterpret_cast<float *>(p);
-    p += up16((size_t)S * 4);
+    w.dot = reinterpret_cast<float *>(p);
+    p += up16((size_t)S * parts * 4);
     w.seen = reinterpret_cast<int *>(p);
     p += up16((size_t)rows * 4);
     w.counts = reinterpret_cast<int *>(p);
@@ -476,209 +790,277 @@ __device__ __forceinline__ void sequence(const int32_t *off, int s, int T, int &
     bad |= a != lo || b != hi;
 }
 
-// The first sequence that ends behind token t (S if none does).
-__device__ __forceinline__ int first_sequence(const int32_t *off, int S, int t)
+// The sequence that token t is in, or -1: the first that ends behind t, if it
+// begins in time. The token's 16 lanes look at 16 offsets at a time.
+__device__ __forceinline__ int sequence_of(const int32_t *off, int S, int t)
 {
     if (!off)
         return 0;
-    int lo = 0, hi = S;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (off[mid + 1] > t)
-            hi = mid;
-        else
-            lo = mid + 1;
+    int lo = 0, n = S;
+    while (__ballot(n > 0)) {
+        const int step = (n + kRow - 1) / kRow, at = (row_lane() + 1) * step - 1;
+        const bool before = n > 0 && at < n && off[lo + at + 1] <= t;
+        const int c = __builtin_popcount(row_ballot(before)) * step;
+        lo += c;
+        n = n > 0 ? min(n - c, step - 1) : 0;
     }
-    return lo;
+    return lo < S && off[lo] <= t ? lo : -1;
 }
 
-__device__ __forceinline__ float block_sum(float v, float *meet)
+template <int N, bool SIGMOID>
+__global__ __launch_bounds__(Run<N>::kThreads) void balance_kernel(BalanceArgs a, bool wide)
 {
-    v = wave_sum(v);
-    __syncthreads();
-    if (lane_id() == 0)
-        meet[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0f;
-    for (int w = 0; w < (int)blockDim.x >> 6; ++w)
-        v += meet[w];
-    return v;
-}
-
-template <int V, bool SIGMOID>
-__global__ __launch_bounds__(kWave *kRunWaves) void balance_kernel(BalanceArgs a, bool wide)
-{
-    __shared__ int cnt[V * kWave];
-    __shared__ float part[kRunWaves][V * kWave];
-    __shared__ int n_seen[kRunWaves];
-    __shared__ float meet[kRunWaves];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = lane_id(), e0 = lane * V;
+    typedef Run<N> R;
+    __shared__ float share[R::kTokensOfRun][R::kColumns];
+    __shared__ uint32_t cnt[R::kTokensOfRun][R::kColumns / 2];  // two experts a word
+    __shared__ int seq[R::kTokensOfRun];
+    __shared__ int has_route[R::kTokensOfRun];
+    __shared__ float seq_loss[R::kTokensOfRun];
+    const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
+    const int mine = tid / kRow, i = row_lane();  // this token of the run
     const BalanceWs ws = balance_ws(a.ws, a.T, a.E, a.S);
-    const bool whole = gridDim.x == 1;  // the one run of the batch: outputs at once
-    const int c0 = blockIdx.x * kRun, c1 = min(c0 + kRun, a.T);
-    bool bad_logit = false, bad_off = false, bad_route = false;
+    const bool whole = gridDim.x == 1;
+    const int64_t t = (int64_t)blockIdx.x * R::kTokensOfRun + mine;
+    bool bad_off = false, bad_logit = false, bad_route = false;
+
+    // what is read of the token, before its sequence is known
+    constexpr int kPer = 2;  // entries of a lane: i, i + 16
+    int64_t e[kPer];
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+        const int k = i + m * kRow;
+        e[m] = t < a.T && k < a.K ? a.topk_idx[t * a.K + k] : -1;
+    }
+    float l[N];
+    load_logits<N>(a.logits + (size_t)t * a.E, a.E, wide, t < a.T, l, bad_logit);
+    for (int c = tid; c < R::kTokensOfRun * R::kColumns / 2; c += R::kThreads)
+        (&cnt[0][0])[c] = 0;
+    int s = sequence_of(a.seq_off, a.S, (int)min(t, (int64_t)a.T));
+    s = t < a.T ? s : -1;
+    bool named[kPer];
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+        named[m] = s >= 0 && e[m] >= 0 && e[m] < a.E;
+        bad_route |= s >= 0 && (e[m] < -1 || e[m] >= a.E);
+    }
+    const bool seen = row_ballot(named[0] || named[1]) != 0;
+    bad_logit = bad_logit && seen;
+    if (i == 0) {
+        seq[mine] = s;
+        has_route[mine] = seen;
+    }
     if (blockIdx.x == 0) {
         if (tid == 0)
             *ws.done = 0;
-        // every sequence's offsets are looked at once
-        for (int s = tid; s < a.S; s += blockDim.x) {
+        for (int q = tid; q < a.S; q += R::kThreads) {
             int lo, hi;
-            sequence(a.seq_off, s, a.T, lo, hi, bad_off);
+            sequence(a.seq_off, q, a.T, lo, hi, bad_off);
+            if (whole && lo == hi) {  // without tokens
+                a.num_tokens[q] = 0;
+                for (int c = 0; c < a.E; ++c) {
+                    a.counts[(size_t)q * a.E + c] = 0;
+                    a.probs[(size_t)q * a.E + c] = 0.0f;
+                }
+            }
         }
     }
-    float total = 0.0f;
-    int some = 0;
-    for (int s = whole ? 0 : first_sequence(a.seq_off, a.S, c0); s < a.S; ++s) {
-        int lo, hi;
-        sequence(a.seq_off, s, a.T, lo, hi, bad_off);
-        if (!whole && lo >= c1)
-            break;
-        lo = max(lo, c0);
-        hi = min(hi, c1);
-        for (int e = tid; e < V * kWave; e += blockDim.x)
-            cnt[e] = 0;
-        __syncthreads();
-        float p[V];
+    {
+        float p[N];
+        shares_of<N, SIGMOID>(l, p, nullptr);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            p[j] = 0.0f;
-        int seen = 0;
-        for (int t = lo + wave; t < hi; t += kRunWaves) {
-            const int64_t e = lane < a.K ? a.topk_idx[(int64_t)t * a.K + lane] : -1;
-            bad_route |= e < -1 || e >= a.E;
-            const bool named = e >= 0 && e < a.E;
-            if (named)
-                atomicAdd(&cnt[(int)e], 1);
-            if (!__ballot(named))
-                continue;
-            ++seen;
-            float l[V], sc[V];
-            load_logits<V>(a.logits + (size_t)t * a.E, a.E, wide, l, bad_logit);
-            const float sum = raw_scores<V, SIGMOID>(l, sc);
-            const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+        for (int j = 0; j < N; j += 4)
+            *reinterpret_cast<float4 *>(&share[mine][expert(j)]) =
+                seen ? float4{p[j], p[j + 1], p[j + 2], p[j + 3]}
+                     : float4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __syncthreads();
+    // the run's sequences: bit b of starts is set where token b's is another
+    // than the one's before it
+    const int sq = lane < R::kTokensOfRun ? seq[lane] : -2;
+    const int before = lane == 0 ? -2 : seq[lane < R::kTokensOfRun ? lane - 1 : 0];
+    const uint64_t starts =
+        uniform64(__ballot(lane < R::kTokensOfRun && (lane == 0 || sq != before)));
+    const uint64_t routed = uniform64(__ballot(lane < R::kTokensOfRun && has_route[lane]));
+    const int segments = __builtin_popcountll(starts);
+    const int segment = __builtin_popcountll(starts & lanes_below(mine + 1)) - 1;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                p[j] = __builtin_fmaf(sc[j], r, p[j]);
+    for (int m = 0; m < kPer; ++m)
+        if (named[m])
+            atomicAdd(&cnt[segment][(int)e[m] >> 1], (e[m] & 1) ? 0x10000u : 1u);
+    // sums over the tokens of a sequence, a part of the run each; a sum is left
+    // in the place of its first token
+    const int col = tid % R::kColumns, part = tid / R::kColumns;
+    if (part < R::kShares) {
+        float q = 0.0f;
+        int first = part * R::kShare;
+#pragma unroll
+        for (int b = 0; b < R::kShare; ++b) {
+            const int at = part * R::kShare + b;
+            const float v = share[at][col];
+            if (b > 0 && (starts >> at & 1)) {
+                share[first][col] = q;
+                first = at;
+                q = 0.0f;
+            }
+            q += v;
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            part[wave][e0 + j] = p[j];
-        if (lane == 0)
-            n_seen[wave] = seen;
-        __syncthreads();
-        int n = 0;
-        for (int w = 0; w < kRunWaves; ++w)
-            n += n_seen[w];
+        share[first][col] = q;
+    }
+    __syncthreads();
+    for (int g = wave; g < segments; g += R::kWaves) {
+        // tokens [b0, b1) of the run
+        uint64_t rest = starts;
+        for (int d = 0; d < g; ++d)
+            rest &= rest - 1;
+        const int b0 = __builtin_ctzll(rest);
+        rest &= rest - 1;
+        const int b1 = rest ? __builtin_ctzll(rest) : R::kTokensOfRun;
+        const int sg = seq[b0];
+        if (sg < 0) {
+            if (lane == 0)
+                seq_loss[g] = -1.0f;
+            continue;
+        }
+        const int n = __builtin_popcountll(routed >> b0 << b0 & (b1 == 64 ? ~0ull : ~(~0ull << b1)));
+        const size_t out = (size_t)(whole ? sg : blockIdx.x + sg) * a.E;
         float dot = 0.0f;
-        for (int e = tid; e < a.E; e += blockDim.x) {
-            float q = 0.0f;
-            for (int w = 0; w < kRunWaves; ++w)
-                q += part[w][e];
+        for (int c = lane; c < a.E; c += kWave) {
+            float q = share[b0][c];
+            for (int b = (b0 / R::kShare + 1) * R::kShare; b < b1; b += R::kShare)
+                q += share[b][c];
+            const int k = cnt[g][c >> 1] >> ((c & 1) * 16) & 0xFFFF;
             if (whole) {
                 q = n ? q / (float)n : 0.0f;
-                a.counts[(size_t)s * a.E + e] = cnt[e];
-                a.probs[(size_t)s * a.E + e] = q;
-                dot = __builtin_fmaf((float)cnt[e], q, dot);
+                a.counts[out + c] = k;
+                a.probs[out + c] = q;
+                dot = __builtin_fmaf((float)k, q, dot);
             } else {
-                const size_t row = (size_t)(blockIdx.x + s) * a.E + e;
-                ws.counts[row] = cnt[e];
-                ws.probs[row] = q;
+                ws.counts[out + c] = k;
+                ws.probs[out + c] = q;
             }
         }
-        if (whole) {
-            dot = block_sum(dot, meet);
-            if (n) {
-                total += dot * ((float)a.E / ((float)a.K * (float)n));
-                ++some;
-            }
-            if (tid == 0)
-                a.num_tokens[s] = n;
-        } else if (tid == 0) {
-            ws.seen[blockIdx.x + s] = n;
+        dot = wave_sum(dot);
+        if (lane == 0) {
+            seq_loss[g] = n ? dot * ((float)a.E / ((float)a.K * (float)n)) : -1.0f;
+            if (whole)
+                a.num_tokens[sg] = n;
+            else
+                ws.seen[blockIdx.x + sg] = n;
         }
-        __syncthreads();
     }
-    if (whole && tid == 0) {
-        a.num_tokens[a.S] = some;
-        a.loss[0] = some ? total / (float)some : 0.0f;
+    if (whole) {
+        __syncthreads();
+        if (tid == 0) {
+            float total = 0.0f;
+            int some = 0;
+            for (int g = 0; g < segments; ++g)
+                if (seq_loss[g] >= 0.0f) {  // of a sequence with tokens
+                    total += seq_loss[g];
+                    ++some;
+                }
+            a.num_tokens[a.S] = some;
+            a.loss[0] = some ? total / (float)some : 0.0f;
+        }
     }
     if (bad_logit || bad_off || bad_route)
         flag_error(a.err, (bad_logit ? EPX_DEV_BAD_LOGIT : 0) | (bad_off ? EPX_DEV_OVERFLOW : 0) |
                               (bad_route ? EPX_DEV_BAD_ROUTE : 0));
 }
 
-__global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArgs a, int lanes)
+// Tokens of sequence s that count: the sum of its rows' numbers.
+__device__ __forceinline__ int tokens_seen(const BalanceWs &ws, int s, int r0, int r1)
 {
-    __shared__ float meet[kFinalThreads / kWave];
-    __shared__ float part[kFinalThreads];
-    __shared__ int part_n[kFinalThreads];
-    __shared__ int n_shared;
+    int n = 0;
+    for (int r = r0 + lane_id(); r < r1; r += kWave)
+        n += ws.seen[r + s];
+    return __builtin_amdgcn_readlane(wave_inclusive_sum(n), 63);
+}
+
+__global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArgs a, int parts)
+{
+    constexpr int kShares = kFinalThreads / kFinalColumns;  // waves: they share the rows
+    __shared__ float sum_p[kShares][kFinalColumns];
+    __shared__ int sum_c[kShares][kFinalColumns];
+    __shared__ float total_w[kShares];
+    __shared__ int some_w[kShares];
     __shared__ bool last;
-    const int s = blockIdx.x, tid = threadIdx.x;
+    const int s = blockIdx.x / parts, part = blockIdx.x - s * parts, tid = threadIdx.x;
+    const int wave = tid / kWave, lane = lane_id(), e = part * kFinalColumns + lane;
+    const int per = run_tokens(a.E);
     const BalanceWs ws = balance_ws(a.ws, a.T, a.E, a.S);
     int lo, hi;
     bool bad = false;
     sequence(a.seq_off, s, a.T, lo, hi, bad);
-    const int r0 = hi > lo ? lo / kRun : 0, r1 = hi > lo ? (hi - 1) / kRun + 1 : 0;
-    if (tid < kWave) {
-        int n = 0;
-        for (int r = r0 + tid; r < r1; r += kWave)
-            n += ws.seen[r + s];
-        n = __builtin_amdgcn_readlane(wave_inclusive_sum(n), 63);
-        if (tid == 0)
-            n_shared = n;
-    }
-    // `lanes` threads per share of the runs, an expert each
-    const int share = tid / lanes, shares = kFinalThreads / lanes, e = tid % lanes;
+    const int r0 = hi > lo ? lo / per : 0, r1 = hi > lo ? (hi - 1) / per + 1 : 0;
     float q = 0.0f;
     int c = 0;
     if (e < a.E) {
 #pragma unroll 8
-        for (int r = r0 + share; r < r1; r += shares) {
+        for (int r = r0 + wave; r < r1; r += kShares) {
             q += ws.probs[(size_t)(r + s) * a.E + e];
             c += ws.counts[(size_t)(r + s) * a.E + e];
         }
     }
-    part[tid] = q;
-    part_n[tid] = c;
+    const int n = tokens_seen(ws, s, r0, r1);
+    sum_p[wave][lane] = q;
+    sum_c[wave][lane] = c;
     __syncthreads();
-    const int n = n_shared;
-    float dot = 0.0f;
-    if (share == 0 && e < a.E) {
-        for (int i = 1; i < shares; ++i) {
-            q += part[i * lanes + e];
-            c += part_n[i * lanes + e];
+    if (wave == 0) {
+#pragma unroll
+        for (int w = 1; w < kShares; ++w) {
+            q += sum_p[w][lane];
+            c += sum_c[w][lane];
         }
         q = n ? q / (float)n : 0.0f;
-        a.counts[(size_t)s * a.E + e] = c;
-        a.probs[(size_t)s * a.E + e] = q;
-        dot = (float)c * q;
-    }
-    dot = block_sum(dot, meet);
-    if (tid == 0) {
-        a.num_tokens[s] = n;
-        const float loss = n ? dot * ((float)a.E / ((float)a.K * (float)n)) : 0.0f;
-        __hip_atomic_store(&ws.seq_loss[s], n ? loss : -1.0f, __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
-        last = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-               gridDim.x - 1;
+        if (e < a.E) {
+            a.counts[(size_t)s * a.E + e] = c;
+            a.probs[(size_t)s * a.E + e] = q;
+        }
+        const float dot = wave_sum((float)c * q);
+        if (lane == 0) {
+            if (part == 0)
+                a.num_tokens[s] = n;
+            // -1 marks a sequence without tokens (the sums are not negative)
+            __hip_atomic_store(&ws.dot[blockIdx.x],
+                               n ? dot * ((float)a.E / ((float)a.K * (float)n)) : -1.0f,
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            // the sum has left this XCD's L2 (a device-coherent store, waited for)
+            // before the block counts itself; nothing else is handed over, so
+            // the L2 need not be written back
+            __builtin_amdgcn_s_waitcnt(0);
+            last = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+        }
     }
     __syncthreads();
     if (!last)
         return;
-    // losses are sums of products that are not negative: -1 marks an empty sequence
-    float sum = 0.0f, some = 0.0f;
-    for (int i = tid; i < a.S; i += kFinalThreads) {
-        const float v = __hip_atomic_load(&ws.seq_loss[i], __ATOMIC_RELAXED,
-                                          __HIP_MEMORY_SCOPE_AGENT);
-        sum += v >= 0.0f ? v : 0.0f;
-        some += v >= 0.0f ? 1.0f : 0.0f;
+    float total = 0.0f;
+    int some = 0;
+    for (int q = tid; q < a.S; q += kFinalThreads) {
+        float v = 0.0f;
+        for (int p = 0; p < parts; ++p)
+            v += __hip_atomic_load(&ws.dot[q * parts + p], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        total += v >= 0.0f ? v : 0.0f;
+        some += v >= 0.0f;
     }
-    sum = block_sum(sum, meet);
-    some = block_sum(some, meet);
+    total = wave_sum(total);
+    some = __builtin_amdgcn_readlane(wave_inclusive_sum(some), 63);
+    if (lane == 0) {
+        total_w[wave] = total;
+        some_w[wave] = some;
+    }
+    __syncthreads();
     if (tid == 0) {
-        a.num_tokens[a.S] = (int)some;
-        a.loss[0] = some > 0.0f ? sum / some : 0.0f;
+        total = 0.0f;
+        some = 0;
+        for (int w = 0; w < kShares; ++w) {
+            total += total_w[w];
+            some += some_w[w];
+        }
+        a.num_tokens[a.S] = some;
+        a.loss[0] = some ? total / (float)some : 0.0f;
     }
 }
 
@@ -691,7 +1073,8 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
 //   else                softmax dl_e += p_e (D_e - sum p D), D = c d at the
 //                       chosen; sigmoid dl_k += c d_k s_k (1 - s_k),
 //   loss                dl_e += p_e g_e (a_e - sum p a),
-// where g is 1 for softmax and 1 - s for sigmoid.
+// where g is 1 for softmax and 1 - s for sigmoid. The entries' values reach
+// their experts' lanes through LDS.
 
 template <bool SIGMOID>
 __device__ __forceinline__ float slope(float l)
@@ -702,167 +1085,235 @@ __device__ __forceinline__ float slope(float l)
     return (l >= 0.0f ? t : 1.0f) / (1.0f + t);
 }
 
-template <int V, bool SIGMOID, bool NORM>
-__global__ __launch_bounds__(kWave *kTokens) void route_backward_kernel(RouteBwdArgs a, bool wide)
+template <int N, bool SIGMOID>
+__global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, bool wide,
+                                                               bool wide_counts, bool wide_out,
+                                                               bool normalize)
 {
-    const int lane = lane_id(), e0 = lane * V;
-    const int64_t t = (int64_t)blockIdx.x * kTokens + (threadIdx.x >> 6);
-    if (t >= a.T)
-        return;
-    bool bad = false;
-    float l[V], dl[V];
+    __shared__ float at_expert[kTokens][kRow * N];
+    constexpr int kPer = 2;  // entries of a lane: i, i + 16
+    const int row = lane_id() / kRow, i = row_lane();
+    const int64_t t = (int64_t)blockIdx.x * kTokens + row;
+    const bool live = t < a.T;
+    bool bad = false, bad_route = false;
+    int e[kPer];
+    float d[kPer];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        dl[j] = 0.0f;
-    int64_t e64 = lane < a.K ? a.topk_idx[t * a.K + lane] : -1;
-    float d = lane < a.K && a.dtopk_w ? a.dtopk_w[t * a.K + lane] : 0.0f;
-    const bool bad_route = e64 < -1 || e64 >= a.E;
-    const int e = bad_route ? -1 : (int)e64;
-    const uint64_t named = uniform64(__ballot(e >= 0));
-    if (named) {
-        load_logits<V>(a.logits + (size_t)t * a.E, a.E, wide, l, bad);
-        int s = 0;
-        bool inside = a.counts != nullptr;
-        if (a.counts && a.seq_off) {
-            s = first_sequence(a.seq_off, a.S, (int)t);
-            inside = s < a.S && a.seq_off[s] <= t;
-        }
-        // the gradient with respect to the shares, where they are needed
-        const bool shares = inside || (a.dtopk_w && !NORM && !SIGMOID);
-        float D[V];
+    for (int m = 0; m < kPer; ++m) {
+        const int k = i + m * kRow;
+        const int64_t v = live && k < a.K ? a.topk_idx[t * a.K + k] : -1;
+        d[m] = live && k < a.K && a.dtopk_w ? a.dtopk_w[t * a.K + k] : 0.0f;
+        bad_route |= v < -1 || v >= a.E;
+        e[m] = v >= 0 && v < a.E ? (int)v : -1;
+    }
+    float l[N];
+    load_logits<N>(a.logits + (size_t)t * a.E, a.E, wide, live, l, bad);
+    const bool routed = row_ballot(e[0] >= 0 || e[1] >= 0) != 0;
+    bad = bad && routed;
+    // the gradients with respect to shares (D) and logits (dl)
+    float D[N], dl[N];
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            D[j] = 0.0f;
-        if (inside) {
+    for (int j = 0; j < N; ++j)
+        D[j] = dl[j] = 0.0f;
+    bool shares = a.dtopk_w && !normalize && !SIGMOID;
+    if (a.counts) {
+        const int s = sequence_of(a.seq_off, a.S, (int)min(t, (int64_t)a.T));
+        if (s >= 0 && routed) {
             const float n = (float)a.num_tokens[s];
             const float c = n > 0.0f ? a.dloss[0] * ((float)a.E / (float)a.K) /
                                            (float)max(a.num_tokens[a.S], 1) / (n * n)
                                      : 0.0f;
+            const int32_t *cnt = a.counts + (size_t)s * a.E;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (e0 + j < a.E)
-                    D[j] = c * (float)a.counts[(size_t)s * a.E + e0 + j];
-        }
-        float g = 0.0f;  // of this lane's entry, added to its expert below
-        if (a.dtopk_w) {
-            float lk = -kInf;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float o = __shfl(l[j], (e < 0 ? 0 : e) / V, kWave);
-                if (e >= 0 && e % V == j)
-                    lk = o;
-            }
-            d = e >= 0 ? d * a.scale : 0.0f;
-            if constexpr (NORM) {
-                const float n = raw_score<SIGMOID>(lk, score_ref<SIGMOID>(wave_max_float(lk)));
-                const float sum = wave_sum(n);
-                const float q = sum > 0.0f ? n / sum : 0.0f;
-                g = q * (d - wave_sum(q * d));
-                if (SIGMOID && lk > -kInf)
-                    g *= slope<true>(lk);
-            } else if constexpr (SIGMOID) {
-                g = lk > -kInf ? d * raw_score<true>(lk, 0.0f) * slope<true>(lk) : 0.0f;
-            } else {
-                g = d;
-            }
-            for (uint64_t todo = named; todo; todo &= todo - 1) {
-                const int k = __builtin_ctzll(todo);
-                const int ek = __builtin_amdgcn_readlane(e, k);
-                const float gk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), k));
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (ek == e0 + j) {
-                        if constexpr (!NORM && !SIGMOID)
-                            D[j] += gk;
-                        else
-                            dl[j] += gk;
-                    }
+            for (int j = 0; j < N; j += 4) {
+                const int4 v = load4<int4, int>(cnt, expert(j), a.E, wide_counts, 0);
+                D[j] = c * (float)v.x;
+                D[j + 1] = c * (float)v.y;
+                D[j + 2] = c * (float)v.z;
+                D[j + 3] = c * (float)v.w;
             }
         }
-        if (shares) {
-            float p[V], dot = 0.0f;
-            const float sum = raw_scores<V, SIGMOID>(l, p);
+        shares = true;
+    }
+    if (a.dtopk_w) {
+        float g[kPer], lk[kPer], n[kPer];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                p[j] = sum > 0.0f ? p[j] / sum : 0.0f;
-                dot = __builtin_fmaf(p[j], D[j], dot);
+        for (int m = 0; m < kPer; ++m) {
+            lk[m] = e[m] >= 0 ? a.logits[(size_t)t * a.E + e[m]] : -kInf;
+            lk[m] = lk[m] < kInf ? lk[m] : -kInf;
+            d[m] = e[m] >= 0 ? d[m] * a.scale : 0.0f;
+        }
+        if (normalize) {
+            const float ref = score_ref<SIGMOID>(row_max(fmaxf(lk[0], lk[1])));
+            n[0] = raw_score<SIGMOID>(lk[0], ref);
+            n[1] = raw_score<SIGMOID>(lk[1], ref);
+            const float sum = row_sum(n[0] + n[1]);
+#pragma unroll
+            for (int m = 0; m < kPer; ++m)
+                n[m] = sum > 0.0f ? n[m] / sum : 0.0f;
+            const float mean = row_sum(__builtin_fmaf(n[0], d[0], n[1] * d[1]));
+#pragma unroll
+            for (int m = 0; m < kPer; ++m) {
+                g[m] = n[m] * (d[m] - mean);
+                if (SIGMOID && lk[m] > -kInf)
+                    g[m] *= slope<true>(lk[m]);
             }
-            dot = wave_sum(dot);
+        } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float v = p[j] * (D[j] - dot);
-                if (SIGMOID && l[j] > -kInf)
-                    v *= slope<true>(l[j]);
-                dl[j] += v;
+            for (int m = 0; m < kPer; ++m) {
+                if constexpr (SIGMOID)
+                    g[m] = lk[m] > -kInf ? d[m] * raw_score<true>(lk[m], 0.0f) * slope<true>(lk[m])
+                                         : 0.0f;
+                else
+                    g[m] = d[m];
+            }
+        }
+        float *cell = at_expert[row];
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+            *reinterpret_cast<float4 *>(&cell[expert(j)]) = float4{0.0f, 0.0f, 0.0f, 0.0f};
+        wave_lds();
+        // an expert named twice: one of the two finds the other's mark
+#pragma unroll
+        for (int m = 0; m < kPer; ++m)
+            if (e[m] >= 0)
+                cell[e[m]] = (float)(i + m * kRow);
+        wave_lds();
+        bool twice = false;
+#pragma unroll
+        for (int m = 0; m < kPer; ++m)
+            twice |= e[m] >= 0 && cell[e[m]] != (float)(i + m * kRow);
+        wave_lds();
+        const bool any = __ballot(twice) != 0;
+#pragma unroll
+        for (int m = 0; m < kPer; ++m)
+            if (e[m] >= 0)
+                cell[e[m]] = any ? 0.0f : g[m];
+        wave_lds();
+        if (any) {  // one entry after the other
+            for (int k = 0; k < a.K; ++k) {
+                if (i == k % kRow) {
+                    const int ek = k < kRow ? e[0] : e[1];
+                    if (ek >= 0)
+                        cell[ek] += k < kRow ? g[0] : g[1];
+                }
+                wave_lds();
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(&cell[expert(j)]);
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (!SIGMOID && !normalize)
+                    D[j + q] += f[q];
+                else
+                    dl[j + q] += f[q];
             }
         }
     }
-    float *out = a.dlogits + (size_t)t * a.E;
+    if (shares) {
+        float p[N], slopes[N], dot = 0.0f;
+        shares_of<N, SIGMOID>(l, p, slopes);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (e0 + j < a.E)
-            out[e0 + j] = dl[j];
+        for (int j = 0; j < N; ++j)
+            dot = __builtin_fmaf(p[j], D[j], dot);
+        dot = row_sum(dot);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if constexpr (SIGMOID)
+                p[j] *= slopes[j];
+            dl[j] = __builtin_fmaf(p[j], D[j] - dot, dl[j]);
+        }
+    }
+    if (live) {
+        float *out = a.dlogits + (size_t)t * a.E;
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const int c = expert(j);
+            if (wide_out) {
+                if (c < a.E)
+                    *reinterpret_cast<float4 *>(out + c) =
+                        float4{dl[j], dl[j + 1], dl[j + 2], dl[j + 3]};
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < a.E)
+                        out[c + q] = dl[j + q];
+            }
+        }
+    }
     if (bad || bad_route)
         flag_error(a.err, (bad ? EPX_DEV_BAD_LOGIT : 0) | (bad_route ? EPX_DEV_BAD_ROUTE : 0));
 }
 
-// Rows of logits that lanes read 16 bytes at a time.
-bool wide_rows(const float *p, int E)
+// Rows of E values that lanes take 16 bytes at a time.
+bool wide_rows(const void *p, int E)
 {
     return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-template <int V>
+dim3 token_blocks(int T) { return dim3((unsigned)(((int64_t)T + kTokens - 1) / kTokens)); }
+
+template <int N, int L>
 hipError_t route_for(const RouteArgs &a, bool sigmoid, bool normalize, hipStream_t stream)
 {
-    int P = 1;  // lanes per group
-    while (2 * P * a.G <= kWave)
+    int P = 1;  // lanes of a group
+    while (2 * P * a.G <= kRow)
         P *= 2;
-    const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(kWave * kTokens);
-    const bool wide = wide_rows(a.logits, a.E);
-    if (sigmoid && normalize)
-        hipLaunchKernelGGL((route_kernel<V, true, true>), grid, block, 0, stream, a, wide, P);
-    else if (sigmoid)
-        hipLaunchKernelGGL((route_kernel<V, true, false>), grid, block, 0, stream, a, wide, P);
-    else if (normalize)
-        hipLaunchKernelGGL((route_kernel<V, false, true>), grid, block, 0, stream, a, wide, P);
+    const bool wide = wide_rows(a.logits, a.E), wide_bias = wide_rows(a.bias, a.E);
+    if (sigmoid)
+        hipLaunchKernelGGL((route_kernel<N, L, true>), token_blocks(a.T), dim3(kWave), 0, stream,
+                           a, wide, wide_bias, P, normalize);
     else
-        hipLaunchKernelGGL((route_kernel<V, false, false>), grid, block, 0, stream, a, wide, P);
+        hipLaunchKernelGGL((route_kernel<N, L, false>), token_blocks(a.T), dim3(kWave), 0, stream,
+                           a, wide, wide_bias, P, normalize);
     return hipGetLastError();
 }
 
-template <int V>
+// Lists of 8 experts a lane, or of all the K there may be.
+template <int N>
+hipError_t route_for(const RouteArgs &a, bool sigmoid, bool normalize, hipStream_t stream)
+{
+    return a.K <= 8 ? route_for<N, 8>(a, sigmoid, normalize, stream)
+                    : route_for<N, EPX_MAX_TOPK>(a, sigmoid, normalize, stream);
+}
+
+template <int N>
 hipError_t balance_for(const BalanceArgs &a, bool sigmoid, hipStream_t stream)
 {
-    const int runs = a.T > 0 ? (a.T + kRun - 1) / kRun : 1;
-    const dim3 grid((unsigned)runs), block(kWave * kRunWaves);
+    typedef Run<N> R;
+    const int runs = a.T > 0 ? (int)(((int64_t)a.T + R::kTokensOfRun - 1) / R::kTokensOfRun) : 1;
+    const dim3 grid((unsigned)runs), block(R::kThreads);
     const bool wide = wide_rows(a.logits, a.E);
     if (sigmoid)
-        hipLaunchKernelGGL((balance_kernel<V, true>), grid, block, 0, stream, a, wide);
+        hipLaunchKernelGGL((balance_kernel<N, true>), grid, block, 0, stream, a, wide);
     else
-        hipLaunchKernelGGL((balance_kernel<V, false>), grid, block, 0, stream, a, wide);
-    hipError_t e = hipGetLastError();
+        hipLaunchKernelGGL((balance_kernel<N, false>), grid, block, 0, stream, a, wide);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || runs == 1)
         return e;
-    hipLaunchKernelGGL(balance_final_kernel, dim3((unsigned)a.S), dim3(kFinalThreads), 0, stream,
-                       a, V * kWave);
+    const int parts = (a.E + kFinalColumns - 1) / kFinalColumns;
+    const int64_t blocks = (int64_t)a.S * parts;
+    if (blocks > 0x7FFFFFFF)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL(balance_final_kernel, dim3((unsigned)blocks), dim3(kFinalThreads), 0,
+                       stream, a, parts);
     return hipGetLastError();
 }
 
-template <int V>
+template <int N>
 hipError_t backward_for(const RouteBwdArgs &a, bool sigmoid, bool normalize, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(kWave * kTokens);
-    const bool wide = wide_rows(a.logits, a.E);
-    if (sigmoid && normalize)
-        hipLaunchKernelGGL((route_backward_kernel<V, true, true>), grid, block, 0, stream, a, wide);
-    else if (sigmoid)
-        hipLaunchKernelGGL((route_backward_kernel<V, true, false>), grid, block, 0, stream, a, wide);
-    else if (normalize)
-        hipLaunchKernelGGL((route_backward_kernel<V, false, true>), grid, block, 0, stream, a, wide);
+    const bool wide = wide_rows(a.logits, a.E), wide_out = wide_rows(a.dlogits, a.E);
+    const bool wide_counts = wide_rows(a.counts, a.E);
+    if (sigmoid)
+        hipLaunchKernelGGL((route_backward_kernel<N, true>), token_blocks(a.T), dim3(kWave), 0,
+                           stream, a, wide, wide_counts, wide_out, normalize);
     else
-        hipLaunchKernelGGL((route_backward_kernel<V, false, false>), grid, block, 0, stream, a,
-                           wide);
+        hipLaunchKernelGGL((route_backward_kernel<N, false>), token_blocks(a.T), dim3(kWave), 0,
+                           stream, a, wide, wide_counts, wide_out, normalize);
     return hipGetLastError();
 }
 
@@ -873,29 +1324,30 @@ hipError_t launch_route(const RouteArgs &a, bool sigmoid, bool normalize, hipStr
     if (a.T == 0)
         return hipSuccess;
     if (a.E <= 64)
-        return route_for<1>(a, sigmoid, normalize, stream);
-    if (a.E <= 128)
-        return route_for<2>(a, sigmoid, normalize, stream);
-    if (a.E <= 256)
         return route_for<4>(a, sigmoid, normalize, stream);
-    return route_for<8>(a, sigmoid, normalize, stream);
+    if (a.E <= 128)
+        return route_for<8>(a, sigmoid, normalize, stream);
+    if (a.E <= 256)
+        return route_for<16>(a, sigmoid, normalize, stream);
+    return route_for<32>(a, sigmoid, normalize, stream);
 }
 
 size_t balance_workspace_bytes(int T, int E, int S)
 {
-    const size_t rows = (size_t)balance_rows(T, S);
-    return 16 + up16((size_t)S * 4) + up16(rows * 4) + 2 * up16(rows * E * 4);
+    const size_t rows = (size_t)balance_rows(T, E, S);
+    const size_t parts = (E + kFinalColumns - 1) / kFinalColumns;
+    return 16 + up16((size_t)S * parts * 4) + up16(rows * 4) + 2 * up16(rows * E * 4);
 }
 
 hipError_t launch_balance(const BalanceArgs &a, bool sigmoid, hipStream_t stream)
 {
     if (a.E <= 64)
-        return balance_for<1>(a, sigmoid, stream);
-    if (a.E <= 128)
-        return balance_for<2>(a, sigmoid, stream);
-    if (a.E <= 256)
         return balance_for<4>(a, sigmoid, stream);
-    return balance_for<8>(a, sigmoid, stream);
+    if (a.E <= 128)
+        return balance_for<8>(a, sigmoid, stream);
+    if (a.E <= 256)
+        return balance_for<16>(a, sigmoid, stream);
+    return balance_for<32>(a, sigmoid, stream);
 }
 
 hipError_t launch_route_backward(const RouteBwdArgs &a, bool sigmoid, bool normalize,
@@ -904,12 +1356,12 @@ hipError_t launch_route_backward(const RouteBwdArgs &a, bool sigmoid, bool norma
     if (a.T == 0)
         return hipSuccess;
     if (a.E <= 64)
-        return backward_for<1>(a, sigmoid, normalize, stream);
-    if (a.E <= 128)
-        return backward_for<2>(a, sigmoid, normalize, stream);
-    if (a.E <= 256)
         return backward_for<4>(a, sigmoid, normalize, stream);
-    return backward_for<8>(a, sigmoid, normalize, stream);
+    if (a.E <= 128)
+        return backward_for<8>(a, sigmoid, normalize, stream);
+    if (a.E <= 256)
+        return backward_for<16>(a, sigmoid, normalize, stream);
+    return backward_for<32>(a, sigmoid, normalize, stream);
 }
 
 }  // namespace epx
