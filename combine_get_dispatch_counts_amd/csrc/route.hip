@@ -24,43 +24,42 @@ __device__ __forceinline__ int row_lane() { return threadIdx.x & (kRow - 1); }
 // The expert of a lane's j-th logit.
 __device__ __forceinline__ int expert(int j) { return 4 * (row_lane() + kRow * (j >> 2)) + (j & 3); }
 
-// Four values of a row from its element e on, `none` past its end. wide: E % 4
-// == 0 and rows of whole 16-byte pieces.
-template <typename V4, typename V>
-__device__ __forceinline__ V4 load4(const V *row, int e, int E, bool wide, V none)
+// A lane's N of a row's E values (0 where it has no expert). No load is
+// guarded: a lane without an expert reads another of the row's, so the loads
+// go out together. wide: E % 4 == 0 and rows of whole 16-byte pieces.
+template <int N, typename V4, typename V>
+__device__ __forceinline__ void load_row(const V *row, int E, bool wide, V (&v)[N])
 {
-    V4 q = {none, none, none, none};
-    if (e < E) {
-        if (wide) {
-            q = *reinterpret_cast<const V4 *>(row + e);
-        } else {
-            q.x = row[e];
-            if (e + 1 < E)
-                q.y = row[e + 1];
-            if (e + 2 < E)
-                q.z = row[e + 2];
-            if (e + 3 < E)
-                q.w = row[e + 3];
+    if (wide) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const V4 q = *reinterpret_cast<const V4 *>(row + min(expert(j), E - 4));
+            v[j] = q.x;
+            v[j + 1] = q.y;
+            v[j + 2] = q.z;
+            v[j + 3] = q.w;
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] = row[min(expert(j), E - 1)];
     }
-    return q;
 }
 
-// A token's logits: -inf where the lane has no expert, and for a NaN or +inf,
-// which sets bad.
+// A token's logits: -inf where the lane has no expert or the token is not
+// live, and for a NaN or +inf, which sets bad.
 template <int N>
 __device__ __forceinline__ void load_logits(const float *row, int E, bool wide, bool live,
                                             float (&l)[N], bool &bad)
 {
-    bool odd = false;
+    load_row<N, float4, float>(row, E, wide, l);
+    const int end = live ? E : 0;
+    if (__ballot(end != kRow * N)) {
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-        const float4 q = load4<float4, float>(row, live ? expert(j) : E, E, wide, -kInf);
-        l[j] = q.x;
-        l[j + 1] = q.y;
-        l[j + 2] = q.z;
-        l[j + 3] = q.w;
+        for (int j = 0; j < N; ++j)
+            l[j] = expert(j) < end ? l[j] : -kInf;
     }
+    bool odd = false;
 #pragma unroll
     for (int j = 0; j < N; ++j)
         odd |= !(l[j] < kInf);
@@ -396,7 +395,7 @@ struct Exact {
 
 // One token's groups in 64 bits by the whole wave: bit g for a group that stays.
 template <int N, int L, bool SIGMOID>
-__device__ __noinline__ uint64_t groups64(const RouteArgs &a, int64_t t, RouteLds<N, L> &lds)
+__device__ __noinline__ uint64_t groups64(RouteArgs a, int64_t t, RouteLds<N, L> &lds)
 {
     const Exact<SIGMOID> exact(a, t);
     const int lane = lane_id();
@@ -436,7 +435,7 @@ __device__ __noinline__ uint64_t groups64(const RouteArgs &a, int64_t t, RouteLd
 // One token's choice in 64 bits by the whole wave, among n candidates: chosen[r]
 // is the r-th expert's number, or ~0.
 template <int N, int L, bool SIGMOID>
-__device__ __noinline__ void choose64(const RouteArgs &a, int64_t t, int n, RouteLds<N, L> &lds,
+__device__ __noinline__ void choose64(RouteArgs a, int64_t t, int n, RouteLds<N, L> &lds,
                                       uint32_t *chosen)
 {
     const int lane = lane_id();
@@ -474,8 +473,9 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
     __shared__ RouteLds<N, L> lds;
     const int row = lane_id() / kRow, i = row_lane();
     const int64_t t = (int64_t)blockIdx.x * kTokens + row;
-    const bool live = t < a.T && (!a.mask || a.mask[t]);
-    const float *logits = a.logits + (size_t)t * a.E;
+    const int64_t tc = min(t, (int64_t)a.T - 1);  // what is read in place of a token behind the last
+    const bool live = t < a.T && (!a.mask || a.mask[tc]);
+    const float *logits = a.logits + (size_t)tc * a.E;
     float l[N];
     bool bad = false;
     load_logits<N>(logits, a.E, wide, live, l, bad);
@@ -510,27 +510,22 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
         }
         if (a.bias) {
             bool odd = false;
-            float m = 0.0f;
+            float b[N], m = 0.0f;
+            load_row<N, float4, float>(a.bias, a.E, wide_bias, b);
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                const float4 q = load4<float4, float>(a.bias, expert(j), a.E, wide_bias, 0.0f);
-                const float b[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    key[j + r] += b[r];
-                    odd |= !(fabsf(b[r]) < kInf);
-                    m = fmaxf(m, fabsf(b[r]));
-                }
+            for (int j = 0; j < N; ++j) {
+                key[j] += b[j];
+                odd |= !(fabsf(b[j]) < kInf);
+                m = fmaxf(m, fabsf(b[j]));
             }
             if (__ballot(odd)) {  // -inf: not chosen; NaN, +inf: nor those
                 m = 0.0f;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float b = expert(j) < a.E ? a.bias[expert(j)] : 0.0f;
-                    const bool can = fabsf(b) < kInf;
-                    bad |= live && !(b < kInf);
+                    const bool can = fabsf(b[j]) < kInf;
+                    bad |= live && !(b[j] < kInf);
                     key[j] = can ? key[j] : -kInf;
-                    m = fmaxf(m, can ? fabsf(b) : 0.0f);
+                    m = fmaxf(m, can ? fabsf(b[j]) : 0.0f);
                 }
             }
             most += row_max(m);
@@ -790,21 +785,27 @@ __device__ __forceinline__ void sequence(const int32_t *off, int s, int T, int &
     bad |= a != lo || b != hi;
 }
 
-// The sequence that token t is in, or -1: the first that ends behind t, if it
-// begins in time. The token's 16 lanes look at 16 offsets at a time.
+// The sequence that token t is in, or -1: the offsets that are not above t are
+// the first ones, and the last of them begins it. The token's 16 lanes look at
+// 64 offsets at a time, so that up to 63 sequences take one load's latency.
 __device__ __forceinline__ int sequence_of(const int32_t *off, int S, int t)
 {
     if (!off)
         return 0;
-    int lo = 0, n = S;
+    int lo = 0, n = S + 1;  // offsets [lo, lo + n) are not decided
     while (__ballot(n > 0)) {
-        const int step = (n + kRow - 1) / kRow, at = (row_lane() + 1) * step - 1;
-        const bool before = n > 0 && at < n && off[lo + at + 1] <= t;
-        const int c = __builtin_popcount(row_ballot(before)) * step;
-        lo += c;
-        n = n > 0 ? min(n - c, step - 1) : 0;
+        const int step = (n + 63) >> 6;
+        int c = 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int at = (m * kRow + row_lane() + 1) * step - 1;
+            const int o = off[min(lo + at, S)];
+            c += __builtin_popcount(row_ballot(n > 0 && at < n && o <= t));
+        }
+        lo += c * step;
+        n = n > 0 ? min(n - c * step, step - 1) : 0;
     }
-    return lo < S && off[lo] <= t ? lo : -1;
+    return lo <= S ? lo - 1 : -1;
 }
 
 template <int N, bool SIGMOID>
@@ -832,7 +833,12 @@ __global__ __launch_bounds__(Run<N>::kThreads) void balance_kernel(BalanceArgs a
         e[m] = t < a.T && k < a.K ? a.topk_idx[t * a.K + k] : -1;
     }
     float l[N];
-    load_logits<N>(a.logits + (size_t)t * a.E, a.E, wide, t < a.T, l, bad_logit);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        l[j] = -kInf;
+    if (a.T > 0)
+        load_logits<N>(a.logits + (size_t)min(t, (int64_t)a.T - 1) * a.E, a.E, wide, t < a.T, l,
+                       bad_logit);
     for (int c = tid; c < R::kTokensOfRun * R::kColumns / 2; c += R::kThreads)
         (&cnt[0][0])[c] = 0;
     int s = sequence_of(a.seq_off, a.S, (int)min(t, (int64_t)a.T));
@@ -1107,7 +1113,8 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
         e[m] = v >= 0 && v < a.E ? (int)v : -1;
     }
     float l[N];
-    load_logits<N>(a.logits + (size_t)t * a.E, a.E, wide, live, l, bad);
+    const int64_t tc = min(t, (int64_t)a.T - 1);  // what is read in place of a token behind the last
+    load_logits<N>(a.logits + (size_t)tc * a.E, a.E, wide, live, l, bad);
     const bool routed = row_ballot(e[0] >= 0 || e[1] >= 0) != 0;
     bad = bad && routed;
     // the gradients with respect to shares (D) and logits (dl)
@@ -1123,15 +1130,11 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
             const float c = n > 0.0f ? a.dloss[0] * ((float)a.E / (float)a.K) /
                                            (float)max(a.num_tokens[a.S], 1) / (n * n)
                                      : 0.0f;
-            const int32_t *cnt = a.counts + (size_t)s * a.E;
+            int cnt[N];  // (of experts that there are; the others have no share)
+            load_row<N, int4, int>(a.counts + (size_t)s * a.E, a.E, wide_counts, cnt);
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                const int4 v = load4<int4, int>(cnt, expert(j), a.E, wide_counts, 0);
-                D[j] = c * (float)v.x;
-                D[j + 1] = c * (float)v.y;
-                D[j + 2] = c * (float)v.z;
-                D[j + 3] = c * (float)v.w;
-            }
+            for (int j = 0; j < N; ++j)
+                D[j] = c * (float)cnt[j];
         }
         shares = true;
     }
