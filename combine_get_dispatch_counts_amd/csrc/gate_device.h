@@ -35,28 +35,33 @@ __device__ __forceinline__ float wave_sum(float v)
 
 // Over each 16 adjacent lanes (a row), the result in all 16 of them: rotations
 // pair the same values in every lane, so a sum is the same in each.
+#define EPX_ROW(v, ctrl) __builtin_amdgcn_mov_dpp((int)(v), ctrl, 0xF, 0xF, true)
+
 __device__ __forceinline__ uint32_t row_max(uint32_t v)
 {
-    v = max(v, (uint32_t)EPX_DPP(v, 0, 0x128, 0xF));  // row_ror:8
-    v = max(v, (uint32_t)EPX_DPP(v, 0, 0x124, 0xF));
-    v = max(v, (uint32_t)EPX_DPP(v, 0, 0x122, 0xF));
-    return max(v, (uint32_t)EPX_DPP(v, 0, 0x121, 0xF));
+    v = max(v, (uint32_t)EPX_ROW(v, 0x128));  // row_ror:8
+    v = max(v, (uint32_t)EPX_ROW(v, 0x124));
+    v = max(v, (uint32_t)EPX_ROW(v, 0x122));
+    return max(v, (uint32_t)EPX_ROW(v, 0x121));
 }
 
+// (In assembly: the compiler spends four instructions a step on a maximum of
+// numbers that may be NaN. The two wait states between a vector write and its
+// use by another lane are in the block.)
 __device__ __forceinline__ float row_max(float v)
 {
-#define EPX_STEP(ctrl) v = fmaxf(v, __int_as_float(EPX_DPP(__float_as_int(v), 0, ctrl, 0xF)))
-    EPX_STEP(0x128);
-    EPX_STEP(0x124);
-    EPX_STEP(0x122);
-    EPX_STEP(0x121);
-#undef EPX_STEP
+    asm("s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_ror:4 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_ror:2 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_ror:1 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1"
+        : "+v"(v));
     return v;
 }
 
 __device__ __forceinline__ float row_sum(float v)
 {
-#define EPX_STEP(ctrl) v = v + __int_as_float(EPX_DPP(__float_as_int(v), 0, ctrl, 0xF))
+#define EPX_STEP(ctrl) v = v + __int_as_float(EPX_ROW(__float_as_int(v), ctrl))
     EPX_STEP(0x128);
     EPX_STEP(0x124);
     EPX_STEP(0x122);

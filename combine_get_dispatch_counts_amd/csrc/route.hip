@@ -103,6 +103,22 @@ __device__ __forceinline__ float score_ref(float top)
     return SIGMOID ? fminf(top, 0.0f) : top;
 }
 
+// A score and its slope (softmax: no factor of its gradient, 1; sigmoid
+// 1 - s) of an entry, unnormalised as raw_score; ref is the token's.
+template <bool SIGMOID>
+__device__ __forceinline__ float entry_score(float l, float ref, float &slope)
+{
+    if constexpr (SIGMOID) {
+        const float t = exp_fp32(-fabsf(l));  // 0 for -inf
+        const float r = 1.0f / (1.0f + t), u = t * r;
+        slope = l >= 0.0f ? u : r;
+        return ref < -60.0f ? raw_score<true>(l, ref) : l >= 0.0f ? r : u;
+    } else {
+        slope = 1.0f;
+        return l > -kInf ? exp_fp32(l - ref) : 0.0f;
+    }
+}
+
 // A token's shares p of one, and with `slopes` the factor of their gradient
 // (softmax 1; sigmoid 1 - s). An expert that is not live has p = 0.
 template <int N, bool SIGMOID>
@@ -188,23 +204,20 @@ __device__ __forceinline__ void descend(uint32_t &a, uint32_t &b)
     a = hi;
 }
 
-// Any order -> descending.
+// Any order -> descending: odd-even merges (19 exchanges of 8 words, 63 of 16).
 template <int M>
 __device__ __forceinline__ void sort_words(uint32_t (&w)[M])
 {
 #pragma unroll
-    for (int k = 2; k <= M; k *= 2)
+    for (int p = 1; p < M; p *= 2)
 #pragma unroll
-        for (int j = k / 2; j > 0; j /= 2)
+        for (int k = p; k >= 1; k /= 2)
 #pragma unroll
-            for (int i = 0; i < M; ++i) {
-                const int o = i ^ j;
-                if (o > i) {
-                    if ((i & k) == 0)
-                        descend(w[i], w[o]);
-                    else
-                        descend(w[o], w[i]);
-                }
+            for (int j = 0; j < M; ++j) {
+                // j is the upper of a pair of its merge
+                const int r = j - k % p;
+                if (r >= 0 && (r / k) % 2 == 0 && j + k < M && j / (2 * p) == (j + k) / (2 * p))
+                    descend(w[j], w[j + k]);
             }
 }
 
@@ -263,7 +276,7 @@ __device__ __forceinline__ void merge_lanes(uint32_t (&best)[L])
     uint32_t o[L];
 #pragma unroll
     for (int j = 0; j < L; ++j)
-        o[j] = (uint32_t)EPX_DPP(best[j], 0, CTRL, 0xF);
+        o[j] = (uint32_t)EPX_ROW(best[j], CTRL);
 #pragma unroll
     for (int j = 0; j < L; ++j)
         best[j] = max(best[j], o[L - 1 - j]);
@@ -302,49 +315,55 @@ struct RouteLds {
 // What a wave wrote to LDS is there for its other lanes.
 __device__ __forceinline__ void wave_lds() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// Bits of the groups that stay, at (group * P); near: a kept and a dropped
-// group's scores are within tol of each other. P lanes of a token walk a group
-// of `units` units (P = 1 with more than 16 groups, when a lane has several).
-template <int N, int L>
-__device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, RouteLds<N, L> &lds, int P,
-                                                int units, bool fours, float tol, bool &near)
+// The two largest of x, y and of another's.
+__device__ __forceinline__ void best_two(float &x, float &y, float ox, float oy)
 {
-    const int row = lane_id() / kRow, i = row_lane();
+    y = fmaxf(fmaxf(y, oy), fminf(x, ox));
+    x = fmaxf(x, ox);
+}
+
+// Bits of the groups that stay, at (group << shift); near: a kept and a dropped
+// group's scores are within tol of each other. 2^shift lanes of a token walk a
+// group (one with more than 16 groups, when a lane has several).
+template <int N, int L>
+__device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, RouteLds<N, L> &lds, int shift,
+                                                bool fours, float tol, bool &near)
+{
+    const int row = lane_id() / kRow, i = row_lane(), P = 1 << shift, part = i & (P - 1);
     const float *unit = lds.unit[row];
     float *score = lds.score[row];
-    for (int g = i / P; g < a.G; g += kRow / P) {
+    for (int g0 = 0; g0 < a.G; g0 += kRow >> shift) {
+        const int g = min(g0 + (i >> shift), a.G - 1);
         float x = -kInf, y = -kInf;
-#pragma unroll 4
-        for (int m = i % P; m < units; m += P) {
-            const int u = RouteLds<N, L>::at(g * units + m);
-            const float k = unit[fours ? 2 * u : u];
-            y = fmaxf(y, fminf(x, k));
-            x = fmaxf(x, k);
-            if (fours)
-                y = fmaxf(y, unit[2 * u + 1]);
+        if (fours) {
+            const int units = a.group_size >> 2;
+            for (int m = part; m < units; m += P) {
+                const float2 k = *reinterpret_cast<const float2 *>(
+                    &unit[2 * RouteLds<N, L>::at(g * units + m)]);
+                best_two(x, y, k.x, k.y);
+            }
+        } else {
+            for (int m = part; m < a.group_size; m += P)
+                best_two(x, y, unit[RouteLds<N, L>::at(g * a.group_size + m)], -kInf);
         }
-        for (int d = 1; d < P; d <<= 1) {
-            const float ox = __shfl_xor(x, d, kWave), oy = __shfl_xor(y, d, kWave);
-            y = fmaxf(fmaxf(y, oy), fminf(x, ox));
-            x = fmaxf(x, ox);
-        }
-        if (i % P == 0)
+        for (int d = 1; d < P; d <<= 1)
+            best_two(x, y, __shfl_xor(x, d, kWave), __shfl_xor(y, d, kWave));
+        if (part == 0)
             score[g] = y > -kInf ? x + y : x;
     }
     wave_lds();
     uint64_t bits = 0;
     float lo = kInf, hi = -kInf;
-    for (int g0 = 0; g0 < a.G; g0 += kRow / P) {
-        const int g = g0 + i / P;
+    for (int g0 = 0; g0 < a.G; g0 += kRow >> shift) {
+        const int g = g0 + (i >> shift);
         const float mine = g < a.G ? score[g] : -kInf;
         int rank = 0;
-#pragma unroll 4
         for (int o = 0; o < a.G; ++o) {
             const float s = score[o];
             rank += s > mine || (s == mine && o < g);
         }
         const bool kept = g < a.G && rank < a.top_groups && mine > -kInf;
-        bits |= (uint64_t)row_ballot(kept && i % P == 0) << (g0 * P);
+        bits |= (uint64_t)row_ballot(kept && part == 0) << (g0 << shift);
         lo = kept ? fminf(lo, mine) : lo;
         hi = kept ? hi : fmaxf(hi, mine);
     }
@@ -444,8 +463,12 @@ __device__ __noinline__ void choose64(RouteArgs a, int64_t t, int n, RouteLds<N,
         for (int c = lane; c < n; c += kWave)
             lds.key64[c] = exact.key(lds.candidate[c]);
     } else {  // the logits order
+        const auto logit = [&](int e) {
+            const float l = a.logits[(size_t)t * a.E + e];
+            return l < kInf ? l : -kInf;
+        };
         for (int c = lane; c < n; c += kWave)
-            lds.key64[c] = (double)a.logits[(size_t)t * a.E + lds.candidate[c]];
+            lds.key64[c] = (double)logit(lds.candidate[c]);
     }
     if (lane < L)
         chosen[lane] = ~0u;
@@ -453,6 +476,8 @@ __device__ __noinline__ void choose64(RouteArgs a, int64_t t, int n, RouteLds<N,
     for (int c = lane; c < n; c += kWave) {
         const int e = lds.candidate[c];
         const double k = lds.key64[c];
+        if (!(k > -(double)kInf))  // can not be chosen
+            continue;
         int rank = 0;
 #pragma unroll 4
         for (int o = 0; o < n; ++o) {
@@ -466,8 +491,8 @@ __device__ __noinline__ void choose64(RouteArgs a, int64_t t, int n, RouteLds<N,
 }
 
 template <int N, int L, bool SIGMOID>
-__global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bool wide_bias,
-                                                      int P, bool normalize)
+__global__ __launch_bounds__(kWave, N <= 16 ? 4 : 2) void route_kernel(RouteArgs a, bool wide, bool wide_bias,
+                                                      int shift, bool normalize)
 {
     typedef Word<N> W;
     __shared__ RouteLds<N, L> lds;
@@ -480,12 +505,24 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
     bool bad = false;
     load_logits<N>(logits, a.E, wide, live, l, bad);
     const float top_l = largest(l);
+    float sum_l = 1.0f;  // of the softmax, where the weights need it
+    if (!SIGMOID && !normalize) {
+        sum_l = 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            sum_l += exp_fp32(l[j] - top_l);  // 0 for -inf
+        sum_l = row_sum(sum_l);
+    }
 
     // order values: the logits, or scores with their bias
     float order[N];
     float per_unit = (W::kMost + 1.0f) / kLogitWindow, top = top_l;
     int tol = 0;
     bool near = false;
+    uint64_t kept = 0;  // groups that stay
+    const auto stays = [&](int e) {
+        return kept >> (div_by_magic(e, a.size_mul) << shift & 63) & 1;
+    };
 #pragma unroll
     for (int j = 0; j < N; ++j)
         order[j] = l[j];
@@ -530,37 +567,37 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
             }
             most += row_max(m);
         }
+        float least = l[0];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            key[j] = l[j] > -kInf ? key[j] : -kInf;
-        const float pair = pair_tol<SIGMOID>(best, most);
-        if (a.bias) {
+        for (int j = 1; j < N; ++j)
+            least = fminf(least, l[j]);
+        if (__ballot(!(least > -kInf))) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                order[j] = key[j];
+                key[j] = l[j] > -kInf ? key[j] : -kInf;
         }
+        const float pair = pair_tol<SIGMOID>(best, most);
+        const bool fours = a.group_size % 4 == 0;
         if (a.G > 1) {
-            const bool fours = a.group_size % 4 == 0;
             float *unit = lds.unit[row];
+            if (fours) {
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                if (fours) {
-                    const float x = fmaxf(key[j], key[j + 1]), u = fminf(key[j], key[j + 1]);
-                    const float y = fmaxf(key[j + 2], key[j + 3]), v = fminf(key[j + 2], key[j + 3]);
-                    const int at = 2 * RouteLds<N, L>::at(expert(j) >> 2);
-                    unit[at] = fmaxf(x, y);
-                    unit[at + 1] = fmaxf(fmaxf(u, v), fminf(x, y));
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        unit[RouteLds<N, L>::at(expert(j) + r)] = key[j + r];
+                for (int j = 0; j < N; j += 4) {
+                    float x = fmaxf(key[j], key[j + 1]), y = fminf(key[j], key[j + 1]);
+                    best_two(x, y, fmaxf(key[j + 2], key[j + 3]), fminf(key[j + 2], key[j + 3]));
+                    *reinterpret_cast<float2 *>(
+                        &unit[2 * RouteLds<N, L>::at(expert(j) >> 2)]) = float2{x, y};
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    unit[RouteLds<N, L>::at(expert(j))] = key[j];
             }
             wave_lds();
             // a score is two keys and a rounding
-            uint64_t kept = best_groups<N, L>(
-                a, lds, P, fours ? a.group_size >> 2 : a.group_size, fours, 3.0f * pair, near);
+            kept = best_groups<N, L>(a, lds, shift, fours, 3.0f * pair, near);
             const uint64_t unsure = uniform64(__ballot(near && live));
+#pragma unroll 1
             for (int q = 0; unsure && q < kTokens; ++q) {
                 if (!(unsure >> (q * kRow) & 0xFFFF))
                     continue;
@@ -569,17 +606,28 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
                 if (row == q) {
                     kept = 0;
                     for (; bits; bits &= bits - 1)
-                        kept |= 1ull << (P * __builtin_ctzll(bits));
+                        kept |= 1ull << (__builtin_ctzll(bits) << shift);
                 }
             }
+        }
+        if (a.bias) {
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
+            for (int j = 0; j < N; ++j)
+                order[j] = key[j];
+        }
+        if (a.G > 1) {
+            if (fours) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int g = div_by_magic(expert(j) + (fours ? 0 : r), a.size_mul);
-                    const bool stays = kept >> (P * g & 63) & 1;
-                    order[j + r] = stays && key[j + r] > -kInf ? order[j + r] : -kInf;
+                for (int j = 0; j < N; j += 4) {
+                    const bool s = stays(expert(j));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        order[j + r] = s ? order[j + r] : -kInf;
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    order[j] = stays(expert(j)) ? order[j] : -kInf;
             }
         }
         top = largest(order);
@@ -621,7 +669,7 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (look && w[j] - from < last - from)
-                near |= l[j] != ll || (a.bias && a.bias[expert(j)] != lb);
+                near |= logits[expert(j)] != ll || (a.bias && a.bias[expert(j)] != lb);
     }
     constexpr int kPer = (L + kRow - 1) / kRow;  // entries of a lane: i, i + 16
     int e[kPer];
@@ -641,6 +689,11 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
     }
     const uint64_t again = uniform64(__ballot(near));
     if (again) {
+        // (the compiler is kept from holding what this rare path needs in
+        // registers from before)
+        int experts = a.E;
+        asm volatile("" : "+v"(kept), "+v"(experts));
+#pragma unroll 1
         for (int q = 0; q < kTokens; ++q) {
             if (!(again >> (q * kRow) & 0xFFFF))
                 continue;
@@ -648,7 +701,8 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
             int n = 0;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const bool can = row == q && order[j] > -kInf && (blind || w[j] >= from);
+                const bool can = row == q && expert(j) < experts &&
+                                 (blind ? a.G == 1 || stays(expert(j)) : w[j] >= from);
                 const uint64_t m = uniform64(__ballot(can));
                 if (can)
                     lds.candidate[n + __builtin_popcountll(m & lanes_below(lane_id()))] =
@@ -677,7 +731,8 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
         const float ref = score_ref<SIGMOID>(row_max(m));
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
-            v[q] = raw_score<SIGMOID>(lk[q], ref);
+            float slope;
+            v[q] = entry_score<SIGMOID>(lk[q], ref, slope);
             sum += v[q];
         }
         total = row_sum(sum);
@@ -686,11 +741,7 @@ __global__ __launch_bounds__(kWave) void route_kernel(RouteArgs a, bool wide, bo
         for (int q = 0; q < kPer; ++q)
             v[q] = raw_score<true>(lk[q], 0.0f);
     } else {
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            sum += exp_fp32(l[j] - top_l);  // 0 for -inf
-        total = row_sum(sum);
+        total = sum_l;
 #pragma unroll
         for (int q = 0; q < kPer; ++q)
             v[q] = raw_score<false>(lk[q], top_l);
@@ -812,8 +863,8 @@ template <int N, bool SIGMOID>
 __global__ __launch_bounds__(Run<N>::kThreads) void balance_kernel(BalanceArgs a, bool wide)
 {
     typedef Run<N> R;
-    __shared__ float share[R::kTokensOfRun][R::kColumns];
-    __shared__ uint32_t cnt[R::kTokensOfRun][R::kColumns / 2];  // two experts a word
+    __shared__ __align__(16) float share[R::kTokensOfRun][R::kColumns];
+    __shared__ __align__(16) uint32_t cnt[R::kTokensOfRun][R::kColumns / 2];  // two experts a word
     __shared__ int seq[R::kTokensOfRun];
     __shared__ int has_route[R::kTokensOfRun];
     __shared__ float seq_loss[R::kTokensOfRun];
@@ -839,8 +890,8 @@ __global__ __launch_bounds__(Run<N>::kThreads) void balance_kernel(BalanceArgs a
     if (a.T > 0)
         load_logits<N>(a.logits + (size_t)min(t, (int64_t)a.T - 1) * a.E, a.E, wide, t < a.T, l,
                        bad_logit);
-    for (int c = tid; c < R::kTokensOfRun * R::kColumns / 2; c += R::kThreads)
-        (&cnt[0][0])[c] = 0;
+    for (int c = tid; c < R::kTokensOfRun * R::kColumns / 8; c += R::kThreads)
+        reinterpret_cast<uint4 *>(&cnt[0][0])[c] = uint4{0u, 0u, 0u, 0u};
     int s = sequence_of(a.seq_off, a.S, (int)min(t, (int64_t)a.T));
     s = t < a.T ? s : -1;
     bool named[kPer];
@@ -895,7 +946,8 @@ __global__ __launch_bounds__(Run<N>::kThreads) void balance_kernel(BalanceArgs a
             atomicAdd(&cnt[segment][(int)e[m] >> 1], (e[m] & 1) ? 0x10000u : 1u);
     // sums over the tokens of a sequence, a part of the run each; a sum is left
     // in the place of its first token
-    const int col = tid % R::kColumns, part = tid / R::kColumns;
+    const int col = tid % R::kColumns;
+    const int part = __builtin_amdgcn_readfirstlane(tid / R::kColumns);  // (whole waves)
     if (part < R::kShares) {
         float q = 0.0f;
         int first = part * R::kShare;
@@ -1082,22 +1134,13 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
 // where g is 1 for softmax and 1 - s for sigmoid. The entries' values reach
 // their experts' lanes through LDS.
 
-template <bool SIGMOID>
-__device__ __forceinline__ float slope(float l)
-{
-    if constexpr (!SIGMOID)
-        return 1.0f;
-    const float t = exp_fp32(-fabsf(l));
-    return (l >= 0.0f ? t : 1.0f) / (1.0f + t);
-}
-
-template <int N, bool SIGMOID>
+// kPer: entries of a lane, i and (with more than 16 of them) i + 16.
+template <int N, int kPer, bool SIGMOID>
 __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, bool wide,
                                                                bool wide_counts, bool wide_out,
                                                                bool normalize)
 {
-    __shared__ float at_expert[kTokens][kRow * N];
-    constexpr int kPer = 2;  // entries of a lane: i, i + 16
+    __shared__ __align__(16) float at_expert[kTokens][kRow * N];
     const int row = lane_id() / kRow, i = row_lane();
     const int64_t t = (int64_t)blockIdx.x * kTokens + row;
     const bool live = t < a.T;
@@ -1115,7 +1158,7 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
     float l[N];
     const int64_t tc = min(t, (int64_t)a.T - 1);  // what is read in place of a token behind the last
     load_logits<N>(a.logits + (size_t)tc * a.E, a.E, wide, live, l, bad);
-    const bool routed = row_ballot(e[0] >= 0 || e[1] >= 0) != 0;
+    const bool routed = row_ballot(e[0] >= 0 || (kPer > 1 && e[kPer - 1] >= 0)) != 0;
     bad = bad && routed;
     // the gradients with respect to shares (D) and logits (dl)
     float D[N], dl[N];
@@ -1132,43 +1175,53 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
                                      : 0.0f;
             int cnt[N];  // (of experts that there are; the others have no share)
             load_row<N, int4, int>(a.counts + (size_t)s * a.E, a.E, wide_counts, cnt);
+            // what all shares' gradients have in common is none of the logits',
+            // as the shares sum to one: counts relative to an even spread, so
+            // that nearly equal ones do not cancel in fp32
+            const float even = n * (float)a.K / (float)a.E;
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                D[j] = c * (float)cnt[j];
+                D[j] = c * ((float)cnt[j] - even);
         }
         shares = true;
     }
     if (a.dtopk_w) {
-        float g[kPer], lk[kPer], n[kPer];
+        float g[kPer], lk[kPer];
 #pragma unroll
         for (int m = 0; m < kPer; ++m) {
-            lk[m] = e[m] >= 0 ? a.logits[(size_t)t * a.E + e[m]] : -kInf;
+            lk[m] = e[m] >= 0 ? a.logits[(size_t)tc * a.E + e[m]] : -kInf;
             lk[m] = lk[m] < kInf ? lk[m] : -kInf;
             d[m] = e[m] >= 0 ? d[m] * a.scale : 0.0f;
         }
         if (normalize) {
-            const float ref = score_ref<SIGMOID>(row_max(fmaxf(lk[0], lk[1])));
-            n[0] = raw_score<SIGMOID>(lk[0], ref);
-            n[1] = raw_score<SIGMOID>(lk[1], ref);
-            const float sum = row_sum(n[0] + n[1]);
-#pragma unroll
-            for (int m = 0; m < kPer; ++m)
-                n[m] = sum > 0.0f ? n[m] / sum : 0.0f;
-            const float mean = row_sum(__builtin_fmaf(n[0], d[0], n[1] * d[1]));
+            float n[kPer], slopes[kPer], top = lk[0], sum = 0.0f, mean = 0.0f;
+            if (kPer > 1)
+                top = fmaxf(top, lk[kPer - 1]);
+            const float ref = score_ref<SIGMOID>(row_max(top));
 #pragma unroll
             for (int m = 0; m < kPer; ++m) {
-                g[m] = n[m] * (d[m] - mean);
-                if (SIGMOID && lk[m] > -kInf)
-                    g[m] *= slope<true>(lk[m]);
+                n[m] = entry_score<SIGMOID>(lk[m], ref, slopes[m]);
+                sum += n[m];
             }
+            sum = row_sum(sum);
+#pragma unroll
+            for (int m = 0; m < kPer; ++m) {
+                n[m] = sum > 0.0f ? n[m] / sum : 0.0f;
+                mean = __builtin_fmaf(n[m], d[m], mean);
+            }
+            mean = row_sum(mean);
+#pragma unroll
+            for (int m = 0; m < kPer; ++m)
+                g[m] = n[m] * (d[m] - mean) * slopes[m];
         } else {
 #pragma unroll
             for (int m = 0; m < kPer; ++m) {
-                if constexpr (SIGMOID)
-                    g[m] = lk[m] > -kInf ? d[m] * raw_score<true>(lk[m], 0.0f) * slope<true>(lk[m])
-                                         : 0.0f;
-                else
-                    g[m] = d[m];
+                g[m] = d[m];
+                if constexpr (SIGMOID) {
+                    float slope;
+                    g[m] *= entry_score<true>(lk[m], 0.0f, slope);
+                    g[m] *= slope;
+                }
             }
         }
         float *cell = at_expert[row];
@@ -1196,9 +1249,9 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
         if (any) {  // one entry after the other
             for (int k = 0; k < a.K; ++k) {
                 if (i == k % kRow) {
-                    const int ek = k < kRow ? e[0] : e[1];
+                    const int ek = k < kRow ? e[0] : e[kPer - 1];
                     if (ek >= 0)
-                        cell[ek] += k < kRow ? g[0] : g[1];
+                        cell[ek] += k < kRow ? g[0] : g[kPer - 1];
                 }
                 wave_lds();
             }
@@ -1262,16 +1315,16 @@ dim3 token_blocks(int T) { return dim3((unsigned)(((int64_t)T + kTokens - 1) / k
 template <int N, int L>
 hipError_t route_for(const RouteArgs &a, bool sigmoid, bool normalize, hipStream_t stream)
 {
-    int P = 1;  // lanes of a group
-    while (2 * P * a.G <= kRow)
-        P *= 2;
+    int shift = 0;  // lanes of a group
+    while ((2 << shift) * a.G <= kRow)
+        ++shift;
     const bool wide = wide_rows(a.logits, a.E), wide_bias = wide_rows(a.bias, a.E);
     if (sigmoid)
         hipLaunchKernelGGL((route_kernel<N, L, true>), token_blocks(a.T), dim3(kWave), 0, stream,
-                           a, wide, wide_bias, P, normalize);
+                           a, wide, wide_bias, shift, normalize);
     else
         hipLaunchKernelGGL((route_kernel<N, L, false>), token_blocks(a.T), dim3(kWave), 0, stream,
-                           a, wide, wide_bias, P, normalize);
+                           a, wide, wide_bias, shift, normalize);
     return hipGetLastError();
 }
 
@@ -1306,18 +1359,25 @@ hipError_t balance_for(const BalanceArgs &a, bool sigmoid, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <int N>
+template <int N, int kPer>
 hipError_t backward_for(const RouteBwdArgs &a, bool sigmoid, bool normalize, hipStream_t stream)
 {
     const bool wide = wide_rows(a.logits, a.E), wide_out = wide_rows(a.dlogits, a.E);
     const bool wide_counts = wide_rows(a.counts, a.E);
     if (sigmoid)
-        hipLaunchKernelGGL((route_backward_kernel<N, true>), token_blocks(a.T), dim3(kWave), 0,
-                           stream, a, wide, wide_counts, wide_out, normalize);
+        hipLaunchKernelGGL((route_backward_kernel<N, kPer, true>), token_blocks(a.T), dim3(kWave),
+                           0, stream, a, wide, wide_counts, wide_out, normalize);
     else
-        hipLaunchKernelGGL((route_backward_kernel<N, false>), token_blocks(a.T), dim3(kWave), 0,
-                           stream, a, wide, wide_counts, wide_out, normalize);
+        hipLaunchKernelGGL((route_backward_kernel<N, kPer, false>), token_blocks(a.T), dim3(kWave),
+                           0, stream, a, wide, wide_counts, wide_out, normalize);
     return hipGetLastError();
+}
+
+template <int N>
+hipError_t backward_for(const RouteBwdArgs &a, bool sigmoid, bool normalize, hipStream_t stream)
+{
+    return a.K <= kRow ? backward_for<N, 1>(a, sigmoid, normalize, stream)
+                       : backward_for<N, 2>(a, sigmoid, normalize, stream);
 }
 
 }  // namespace
