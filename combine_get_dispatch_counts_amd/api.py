@@ -798,11 +798,28 @@ def moe_decode(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tens
     return out
 
 
-def _weight(w: torch.Tensor, h: int, dev: torch.device) -> int:
-    """1 if the norm's weight is fp32, 0 if bf16."""
-    f32 = w is not None and w.dtype == torch.float32
-    _need(w, torch.float32 if f32 else torch.bfloat16, "weight", shape=(h,), device=dev)
-    return int(f32)
+def _arg(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tuple,
+         dev: torch.device) -> int:
+    """The address of a tensor that _need takes (with everything right, half
+    of the time that _need and _p take)."""
+    if (t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev.index
+            or not t.is_contiguous()):
+        _need(t, dtype, name, shape=shape, device=dev)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor | None, dtype: torch.dtype, name: str) -> tuple[torch.device, int, int]:
+    """Device and shape of a call's first matrix."""
+    if t is None or t.dtype is not dtype or t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name, 2)
+    T, n = t.shape
+    return t.device, T, n
+
+
+def _weight(w: torch.Tensor, h: int, dev: torch.device) -> tuple[int, int]:
+    """Address of the norm's weight, and 1 if it is fp32, 0 if bf16."""
+    f32 = w is not None and w.dtype is torch.float32
+    return _arg(w, torch.float32 if f32 else torch.bfloat16, "weight", (h,), dev), int(f32)
 
 
 @dataclass
@@ -835,36 +852,45 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     (alloc_norm's, or any tensors of those shapes) avoids allocating and says
     by its members which outputs there are; its residual may be ``residual``
     or ``x`` itself, and its out one of them that its residual is not."""
-    _need(x, torch.bfloat16, "x", 2)
-    dev = x.device
-    T, h = x.shape
-    f32 = _weight(weight, h, dev)
-    if residual is not None:
-        _need(residual, torch.bfloat16, "residual", shape=(T, h), device=dev)
+    dev, T, h = _rows(x, torch.bfloat16, "x")
+    w, f32 = _weight(weight, h, dev)
+    b16, shape = torch.bfloat16, (T, h)
+    r = None if residual is None else _arg(residual, b16, "residual", shape, dev)
     if buf is None:
         buf = alloc_norm(T, h, residual is not None, bf16, fp8, dev)
-    else:
-        if residual is not None:
-            _need(buf.residual, torch.bfloat16, "buf.residual", shape=(T, h), device=dev)
-        elif buf.residual is not None:
-            raise ValueError("buf.residual goes with a residual")
-        if buf.out is not None:
-            _need(buf.out, torch.bfloat16, "buf.out", shape=(T, h), device=dev)
-        if buf.codes is not None:
-            _need(buf.codes, torch.uint8, "buf.codes", shape=(T, h), device=dev)
-            _need(buf.scales, torch.float32, "buf.scales", shape=(T, scale_stride(h)), device=dev)
-        elif buf.scales is not None:
-            raise ValueError("buf.scales goes with buf.codes")
-    if buf.out is None and buf.codes is None:
+    rout = out = codes = scales = None
+    if residual is not None:
+        rout = _arg(buf.residual, b16, "buf.residual", shape, dev)
+    elif buf.residual is not None:
+        raise ValueError("buf.residual goes with a residual")
+    if buf.out is not None:
+        out = _arg(buf.out, b16, "buf.out", shape, dev)
+    if buf.codes is not None:
+        codes = _arg(buf.codes, torch.uint8, "buf.codes", shape, dev)
+        scales = _arg(buf.scales, torch.float32, "buf.scales", (T, (h // 128 + 31) // 32 * 32), dev)
+    elif buf.scales is not None:
+        raise ValueError("buf.scales goes with buf.codes")
+    elif out is None:
         raise ValueError("rms_norm needs out or codes to write")
-    check(_lib.load().epx_rms_norm(_ctx(dev), _p(x), _p(residual), _p(weight), f32, T, h, eps,
-                                   _p(buf.residual), _p(buf.out), _p(buf.codes), _p(buf.scales),
-                                   _stream(dev)), "epx_rms_norm")
+    check(_lib.load().epx_rms_norm(_ctx(dev), x.data_ptr(), r, w, f32, T, h, eps, rout, out, codes,
+                                   scales, _stream(dev)), "epx_rms_norm")
     return buf
 
 
 def rms_norm_backward_workspace(T: int, h: int) -> int:
     return int(_lib.load().epx_rms_norm_backward_workspace(T, h))
+
+
+def _workspace(ws: torch.Tensor | None, nbytes: int, like: torch.Tensor
+               ) -> tuple[torch.Tensor | None, int | None, int]:
+    """The caller's workspace, or one for this call (to be held until the
+    launch), its address and size."""
+    if ws is not None:
+        return ws, ws.data_ptr(), _nbytes(ws, like.device)
+    if nbytes == 0:
+        return None, None, 0
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    return ws, ws.data_ptr(), nbytes
 
 
 def rms_norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
@@ -879,29 +905,21 @@ def rms_norm_backward(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     of its residual alike. ``out`` (dx, dweight; dx may be dout or dresidual)
     and ``workspace`` (rms_norm_backward_workspace(T, h) bytes; calls that
     share one must not overlap) avoid allocating."""
-    _need(x, torch.bfloat16, "x", 2)
-    dev = x.device
-    T, h = x.shape
-    _need(dout, torch.bfloat16, "dout", shape=(T, h), device=dev)
-    f32 = _weight(weight, h, dev)
-    if dresidual is not None:
-        _need(dresidual, torch.bfloat16, "dresidual", shape=(T, h), device=dev)
+    dev, T, h = _rows(x, torch.bfloat16, "x")
+    b16, shape = torch.bfloat16, (T, h)
+    d = _arg(dout, b16, "dout", shape, dev)
+    w, f32 = _weight(weight, h, dev)
+    r = None if dresidual is None else _arg(dresidual, b16, "dresidual", shape, dev)
     if out is None:
-        dx, dweight = torch.empty_like(x), x.new_empty(h, dtype=torch.float32)
-    else:
-        dx, dweight = out
-        _need(dx, torch.bfloat16, "dx", shape=(T, h), device=dev)
-        _need(dweight, torch.float32, "dweight", shape=(h,), device=dev)
-    if workspace is None:
-        ws_bytes = max(rms_norm_backward_workspace(T, h), 16)
-        workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
-    else:
-        ws_bytes = _nbytes(workspace, dev)
-    check(_lib.load().epx_rms_norm_backward(_ctx(dev), _p(dout), _p(x), _p(weight), f32,
-                                            _p(dresidual), T, h, eps, _p(workspace), ws_bytes,
-                                            _p(dx), _p(dweight), _stream(dev)),
-          "epx_rms_norm_backward")
-    return dx, dweight
+        out = torch.empty_like(x), x.new_empty(h, dtype=torch.float32)
+    dx, dweight = out
+    px = _arg(dx, b16, "dx", shape, dev)
+    pw = _arg(dweight, torch.float32, "dweight", (h,), dev)
+    lib = _lib.load()
+    held, ws, ws_bytes = _workspace(workspace, lib.epx_rms_norm_backward_workspace(T, h), x)
+    check(lib.epx_rms_norm_backward(_ctx(dev), d, x.data_ptr(), w, f32, r, T, h, eps, ws, ws_bytes,
+                                    px, pw, _stream(dev)), "epx_rms_norm_backward")
+    return out
 
 
 _SCORING = {"softmax": 0, "sigmoid": 1}
@@ -929,25 +947,21 @@ def route(logits: torch.Tensor, topk: int, scoring: str = "softmax",
     from being chosen; ``mask`` [T] bool (or uint8) is False for padding,
     which gets -1 and 0 everywhere, as entries do for which no expert is
     left. ``out`` (topk_idx, topk_weights) avoids allocating."""
-    _need(logits, torch.float32, "logits", 2)
-    dev = logits.device
-    T, E = logits.shape
+    dev, T, E = _rows(logits, torch.float32, "logits")
+    b = m = None
     if bias is not None:
-        _need(bias, torch.float32, "bias", shape=(E,), device=dev)
+        b = _arg(bias, torch.float32, "bias", (E,), dev)
     if mask is not None:
-        _need(mask, torch.uint8 if mask.dtype == torch.uint8 else torch.bool, "mask", shape=(T,),
-              device=dev)
+        m = _arg(mask, torch.uint8 if mask.dtype is torch.uint8 else torch.bool, "mask", (T,), dev)
     if out is None:
-        idx = logits.new_empty((T, topk), dtype=torch.int64)
-        w = logits.new_empty((T, topk))
-    else:
-        idx, w = out
-        _need(idx, torch.int64, "topk_idx", shape=(T, topk), device=dev)
-        _need(w, torch.float32, "topk_weights", shape=(T, topk), device=dev)
-    check(_lib.load().epx_route(_ctx(dev), _p(logits), _p(bias), _p(mask), T, E, topk,
-                                _scoring(scoring), num_groups, topk_groups, int(normalize), scale,
-                                _p(idx), _p(w), _stream(dev)), "epx_route")
-    return idx, w
+        out = logits.new_empty((T, topk), dtype=torch.int64), logits.new_empty((T, topk))
+    idx, w = out
+    pi = _arg(idx, torch.int64, "topk_idx", (T, topk), dev)
+    pw = _arg(w, torch.float32, "topk_weights", (T, topk), dev)
+    check(_lib.load().epx_route(_ctx(dev), logits.data_ptr(), b, m, T, E, topk, _scoring(scoring),
+                                num_groups, topk_groups, int(normalize), scale, pi, pw,
+                                _stream(dev)), "epx_route")
+    return out
 
 
 @dataclass
@@ -969,13 +983,20 @@ def balance_workspace(T: int, E: int, S: int) -> int:
     return int(_lib.load().epx_balance_workspace(T, E, S))
 
 
-def _sequences(seq_off: torch.Tensor | None, dev: torch.device) -> int:
+def _sequences(seq_off: torch.Tensor | None, dev: torch.device) -> tuple[int | None, int]:
+    """Address of the sequences' offsets and how many there are."""
     if seq_off is None:
-        return 1
+        return None, 1
     _need(seq_off, torch.int32, "seq_off", 1, device=dev)
     if seq_off.numel() < 2:
         raise ValueError("seq_off needs an entry per sequence and one more")
-    return seq_off.numel() - 1
+    return seq_off.data_ptr(), seq_off.numel() - 1
+
+
+def _choice(topk_idx: torch.Tensor, T: int, dev: torch.device) -> tuple[int, int]:
+    """Address of topk_idx and its entries per token."""
+    K = topk_idx.shape[1] if topk_idx is not None and topk_idx.dim() == 2 else 0
+    return _arg(topk_idx, torch.int64, "topk_idx", (T, K), dev), K
 
 
 def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, scoring: str = "softmax",
@@ -989,34 +1010,21 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, scoring: str = "s
     ends (None: one sequence of all tokens). ``out`` (alloc_balance) and
     ``workspace`` (balance_workspace(T, E, S) bytes; calls that share one must
     not overlap) avoid allocating."""
-    _need(logits, torch.float32, "logits", 2)
-    dev = logits.device
-    T, E = logits.shape
-    _need(topk_idx, torch.int64, "topk_idx", 2, device=dev)
-    K = topk_idx.shape[1]
-    _need(topk_idx, torch.int64, "topk_idx", shape=(T, K))
-    S = _sequences(seq_off, dev)
+    dev, T, E = _rows(logits, torch.float32, "logits")
+    idx, K = _choice(topk_idx, T, dev)
+    off, S = _sequences(seq_off, dev)
     if out is None:
         out = alloc_balance(S, E, dev)
-    else:
-        _check_balance(out, S, E, dev)
-        _need(out.loss, torch.float32, "loss", shape=(1,), device=dev)
-        _need(out.probs, torch.float32, "probs", shape=(S, E), device=dev)
-    if workspace is None:
-        ws_bytes = max(balance_workspace(T, E, S), 16)
-        workspace = logits.new_empty(ws_bytes, dtype=torch.uint8)
-    else:
-        ws_bytes = _nbytes(workspace, dev)
-    check(_lib.load().epx_balance_loss(_ctx(dev), _p(logits), _p(topk_idx), _p(seq_off), T, E, K, S,
-                                       _scoring(scoring), _p(out.loss), _p(out.counts),
-                                       _p(out.probs), _p(out.num_tokens), _p(workspace), ws_bytes,
-                                       _stream(dev)), "epx_balance_loss")
+    loss = _arg(out.loss, torch.float32, "loss", (1,), dev)
+    counts = _arg(out.counts, torch.int32, "counts", (S, E), dev)
+    probs = _arg(out.probs, torch.float32, "probs", (S, E), dev)
+    seen = _arg(out.num_tokens, torch.int32, "num_tokens", (S + 1,), dev)
+    lib = _lib.load()
+    held, ws, ws_bytes = _workspace(workspace, lib.epx_balance_workspace(T, E, S), logits)
+    check(lib.epx_balance_loss(_ctx(dev), logits.data_ptr(), idx, off, T, E, K, S,
+                               _scoring(scoring), loss, counts, probs, seen, ws, ws_bytes,
+                               _stream(dev)), "epx_balance_loss")
     return out
-
-
-def _check_balance(b: Balance, S: int, E: int, dev: torch.device) -> None:
-    _need(b.counts, torch.int32, "counts", shape=(S, E), device=dev)
-    _need(b.num_tokens, torch.int32, "num_tokens", shape=(S + 1,), device=dev)
 
 
 def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, scoring: str = "softmax",
@@ -1030,35 +1038,30 @@ def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, scoring: str = 
     on the device, and the ``seq_off`` it was given), or of both in one pass.
     logits, topk_idx, scoring, normalize and scale as in the forward calls;
     the choice and the counts are constants. ``out`` avoids allocating."""
-    _need(logits, torch.float32, "logits", 2)
-    dev = logits.device
-    T, E = logits.shape
-    _need(topk_idx, torch.int64, "topk_idx", 2, device=dev)
-    K = topk_idx.shape[1]
-    _need(topk_idx, torch.int64, "topk_idx", shape=(T, K))
+    dev, T, E = _rows(logits, torch.float32, "logits")
+    idx, K = _choice(topk_idx, T, dev)
     if dtopk_weights is None and balance is None:
         raise ValueError("route_backward needs dtopk_weights, balance or both")
-    if dtopk_weights is not None:
-        _need(dtopk_weights, torch.float32, "dtopk_weights", shape=(T, K), device=dev)
+    d = counts = seen = pl = off = None
     S = 1
+    if dtopk_weights is not None:
+        d = _arg(dtopk_weights, torch.float32, "dtopk_weights", (T, K), dev)
     if balance is not None:
-        S = _sequences(seq_off, dev)
-        _check_balance(balance, S, E, dev)
+        off, S = _sequences(seq_off, dev)
+        counts = _arg(balance.counts, torch.int32, "counts", (S, E), dev)
+        seen = _arg(balance.num_tokens, torch.int32, "num_tokens", (S + 1,), dev)
         _need(dloss, torch.float32, "dloss", device=dev)
         if dloss.numel() != 1:
             raise ValueError(f"dloss has {dloss.numel()} entries, expected 1")
+        pl = dloss.data_ptr()
     elif dloss is not None or seq_off is not None:
         raise ValueError("dloss and seq_off go with balance")
     if out is None:
         out = torch.empty_like(logits)
-    else:
-        _need(out, torch.float32, "out", shape=(T, E), device=dev)
-    counts, seen = (balance.counts, balance.num_tokens) if balance is not None else (None, None)
-    check(_lib.load().epx_route_backward(_ctx(dev), _p(logits), _p(topk_idx), T, E, K,
-                                         _scoring(scoring), int(normalize), scale,
-                                         _p(dtopk_weights), _p(counts), _p(seen), _p(dloss),
-                                         _p(seq_off), S, _p(out), _stream(dev)),
-          "epx_route_backward")
+    dl = _arg(out, torch.float32, "out", (T, E), dev)
+    check(_lib.load().epx_route_backward(_ctx(dev), logits.data_ptr(), idx, T, E, K,
+                                         _scoring(scoring), int(normalize), scale, d, counts, seen,
+                                         pl, off, S, dl, _stream(dev)), "epx_route_backward")
     return out
 
 
@@ -1072,34 +1075,28 @@ def combine_backward(dout: torch.Tensor, expert_out: torch.Tensor | None, pos: t
     (either may be None: that gradient is left out) avoids allocating; without
     d_topk_weights expert_out is not read, but still says how many rows there
     are (None: as many as out[0] has)."""
-    _need(dout, torch.bfloat16, "dout", 2)
-    dev = dout.device
-    T, h = dout.shape
-    _need(pos, torch.int32, "pos", 2, device=dev)
-    K = pos.shape[1]
-    _need(pos, torch.int32, "pos", shape=(T, K))
-    _need(topk_weights, torch.float32, "topk_weights", shape=(T, K), device=dev)
-    dy, dw = out if out is not None else (None, None)
-    rows_of = dy if expert_out is None else expert_out
-    _need(rows_of, torch.bfloat16, "expert_out", 2, device=dev)
-    n = rows_of.shape[0]
-    _need(rows_of, torch.bfloat16, "expert_out", shape=(n, h))
+    dev, T, h = _rows(dout, torch.bfloat16, "dout")
+    K = pos.shape[1] if pos is not None and pos.dim() == 2 else 0
+    p = _arg(pos, torch.int32, "pos", (T, K), dev)
+    w = _arg(topk_weights, torch.float32, "topk_weights", (T, K), dev)
+    rows_of = expert_out if expert_out is not None or out is None else out[0]
+    n = rows_of.shape[0] if rows_of is not None and rows_of.dim() == 2 else 0
+    y = _arg(rows_of, torch.bfloat16, "expert_out", (n, h), dev)
     if out is None:
-        dy = torch.empty_like(expert_out)
-        dw = torch.empty_like(topk_weights)
-    else:
-        if dy is None and dw is None:
-            raise ValueError("combine_backward needs an output")
-        if dy is not None:
-            _need(dy, torch.bfloat16, "d_expert_out", shape=(n, h), device=dev)
-        if dw is not None:
-            _need(dw, torch.float32, "d_topk_weights", shape=(T, K), device=dev)
-            if expert_out is None:
-                raise ValueError("d_topk_weights needs expert_out")
-    check(_lib.load().epx_combine_backward(_ctx(dev), _p(dout), _p(expert_out), n, h,
-                                           _p(topk_weights), _p(pos), T, K, _p(dy), _p(dw),
+        out = torch.empty_like(expert_out), torch.empty_like(topk_weights)
+    dy, dw = out
+    py = pw = None
+    if dy is not None:
+        py = _arg(dy, torch.bfloat16, "d_expert_out", (n, h), dev)
+    if dw is not None:
+        pw = _arg(dw, torch.float32, "d_topk_weights", (T, K), dev)
+        if expert_out is None:
+            raise ValueError("d_topk_weights needs expert_out")
+    elif dy is None:
+        raise ValueError("combine_backward needs an output")
+    check(_lib.load().epx_combine_backward(_ctx(dev), dout.data_ptr(), y, n, h, w, p, T, K, py, pw,
                                            _stream(dev)), "epx_combine_backward")
-    return dy, dw
+    return out
 
 
 __all__ = ["EpxError", "Layout", "Dispatched", "LowLatency", "workspace_size", "ll_size_hint",

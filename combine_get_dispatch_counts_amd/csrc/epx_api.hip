@@ -952,10 +952,13 @@ int epx_balance_loss(epx_ctx *ctx, const float *logits, const int64_t *topk_idx,
         return rc;
     if ((rc = check_router(T, K, E, scoring)) != EPX_OK)
         return rc;
-    if (S < 1 || (!seq_off && S != 1) || !loss || !counts || !probs || !num_tokens || !ws ||
+    if (S < 1 || (!seq_off && S != 1) || !loss || !counts || !probs || !num_tokens ||
         !aligned16(ws) || (T > 0 && (!logits || !topk_idx)))
         return EPX_EINVAL;
-    if (ws_bytes < epx_balance_workspace(T, E, S))
+    const size_t need = epx_balance_workspace(T, E, S);
+    if (need > 0 && !ws)
+        return EPX_EINVAL;
+    if (ws_bytes < need)
         return EPX_ECAPACITY;
     epx::BalanceArgs a{};
     a.logits = logits; a.topk_idx = topk_idx; a.seq_off = seq_off;

@@ -907,7 +907,7 @@ __global__ __launch_bounds__(Run<N>::kThreads) void balance_kernel(BalanceArgs a
         has_route[mine] = seen;
     }
     if (blockIdx.x == 0) {
-        if (tid == 0)
+        if (tid == 0 && !whole)
             *ws.done = 0;
         for (int q = tid; q < a.S; q += R::kThreads) {
             int lo, hi;
@@ -1397,6 +1397,8 @@ hipError_t launch_route(const RouteArgs &a, bool sigmoid, bool normalize, hipStr
 
 size_t balance_workspace_bytes(int T, int E, int S)
 {
+    if (T <= run_tokens(E))  // one run: the first launch alone
+        return 0;
     const size_t rows = (size_t)balance_rows(T, E, S);
     const size_t parts = (E + kFinalColumns - 1) / kFinalColumns;
     return 16 + up16((size_t)S * parts * 4) + up16(rows * 4) + 2 * up16(rows * E * 4);

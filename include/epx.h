@@ -608,7 +608,8 @@ int epx_route(epx_ctx *ctx, const float *logits, const float *bias, const uint8_
               int E, int K, int scoring, int num_groups, int topk_groups, int normalize,
               float scale, int64_t *topk_idx, float *topk_w, hipStream_t stream);
 
-/* Workspace bytes of epx_balance_loss (host). Returns 0 for bad arguments. */
+/* Workspace bytes of epx_balance_loss (host). Returns 0 for bad arguments, and
+ * for batches of few tokens that need none. */
 size_t epx_balance_workspace(int T, int E, int S);
 
 /* Balance loss, per-expert counts and mean shares of S sequences. A token
@@ -622,9 +623,9 @@ size_t epx_balance_workspace(int T, int E, int S);
  *      expert named twice counts twice); seq_off [S+1] int32, sequence s being
  *      tokens [seq_off[s], seq_off[s+1]), or NULL: one sequence of all T
  *      (S = 1). Tokens of no sequence do not count. Offsets that decrease or
- *      leave [0, T] set EPX_DEV_OVERFLOW. ws: epx_balance_workspace bytes,
- *      16-byte aligned, no initial contents; calls that share it must not
- *      overlap.
+ *      leave [0, T] set EPX_DEV_OVERFLOW. ws: epx_balance_workspace bytes
+ *      (may be NULL if that is 0), 16-byte aligned, no initial contents; calls
+ *      that share it must not overlap.
  * Out: loss [1] fp32; counts [S, E] int32 (c_e); probs [S, E] fp32 (P_e);
  *      num_tokens [S+1] int32: n of each sequence, then the number of
  *      sequences with n > 0. Sums are fp32 in a fixed order: the same inputs

@@ -34,9 +34,10 @@ def test_workspaces(lib):
         assert n % (4 * h) == 0 and 1 <= n // (4 * h) <= min(T, 1024)
     for bad in ((0, 8), (-1, 8), (4, 12), (4, 0), (4, 32768 + 8)):
         assert lib.epx_rms_norm_backward_workspace(*bad) == 0
-    small, large = lib.epx_balance_workspace(1, 1, 1), lib.epx_balance_workspace(16384, 256, 24)
-    assert 0 < small < large < 1 << 20 and large > 256 * 256 * 8
-    assert lib.epx_balance_workspace(0, 8, 1) > 0
+    for T, E, S in ((0, 8, 1), (1, 1, 1), (64, 256, 9), (32, 512, 1)):   # one launch
+        assert lib.epx_balance_workspace(T, E, S) == 0
+    assert lib.epx_balance_workspace(65, 8, 1) > 2 * 8 * 8
+    assert 256 * 256 * 8 < lib.epx_balance_workspace(16384, 256, 24) < 1 << 20
     for bad in ((-1, 8, 1), (4, 0, 1), (4, 513, 1), (4, 8, 0)):
         assert lib.epx_balance_workspace(*bad) == 0
 

@@ -761,6 +761,7 @@ def test_binding_refuses():
         (ValueError, lambda: m.route(l, 2, out=(idx[:3], top))),
         (ValueError, lambda: m.route(l.t().contiguous().t(), 2)),
         (ValueError, lambda: m.balance_loss(l, idx[:3])),
+        (ValueError, lambda: m.balance_loss(l, idx.view(-1))),
         (TypeError, lambda: m.balance_loss(l, idx.int())),
         (TypeError, lambda: m.balance_loss(l, idx, seq_off=off.long())),
         (ValueError, lambda: m.balance_loss(l, idx, seq_off=off[:1])),
@@ -796,8 +797,8 @@ def test_binding_refuses():
         (-1, lambda: m.route(l, 2, scale=float("inf"))),
         (-1, lambda: m.route(torch.zeros((1, 513), device=DEV), 2)),
         (-1, lambda: m.route(torch.zeros((1, 40), device=DEV), 33)),
-        (-2, lambda: m.balance_loss(l, idx, workspace=torch.empty(32, dtype=torch.uint8,
-                                                                  device=DEV))),
+        (-2, lambda: m.balance_loss(l.repeat(20, 1), idx.repeat(20, 1),
+                                    workspace=torch.empty(32, dtype=torch.uint8, device=DEV))),
     ]:
         with pytest.raises(m.EpxError) as e:
             call()
@@ -819,9 +820,9 @@ def test_c_abi_refuses():
                 dict(s=p), dict(x=odd), dict(o=odd), dict(w=odd), dict(r=odd, ro=p), dict(h=4)):
         assert norm(**bad) == -1, bad
     assert norm(h=136, c=p, s=p) == -3
-    bal = lambda off=None, S=1, ws=p, loss=p: lib.epx_balance_loss(  # noqa: E731
-        ctx, p, p, off, 0, 8, 2, S, 0, loss, p, p, p, ws, 16384, None)
-    assert bal() == 0
+    bal = lambda off=None, S=1, ws=p, loss=p, T=0: lib.epx_balance_loss(  # noqa: E731
+        ctx, p, p, off, T, 8, 2, S, 0, loss, p, p, p, ws, 16384, None)
+    assert bal() == 0 and bal(ws=None) == 0 and bal(ws=None, T=65) == -1 and bal(T=1 << 20) == -2
     assert bal(S=2) == -1 and bal(S=0) == -1 and bal(ws=odd) == -1 and bal(loss=None) == -1
     back = lambda d=p, c=None, n=None, dl=None, off=None, S=1, sc=0: lib.epx_route_backward(  # noqa: E731
         ctx, p, p, 0, 8, 2, sc, 1, 1.0, d, c, n, dl, off, S, p, None)
