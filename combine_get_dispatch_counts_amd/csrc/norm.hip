@@ -10,9 +10,9 @@
 // Backward, per row, with n = v inv and g = dout w:
 //   dx = dres + inv (g - n mean(g n)),   dw = sum over rows of dout n.
 // mean(g n) = inv mean(g v), so both row sums (v^2 and g v) come from one
-// pass. A block walks rows b, b + blocks, ... with its share of dw in
-// registers and leaves one row of partial sums, which a second launch adds in
-// block order.
+// pass. Groups of waves have a row each and walk the rows with their share of
+// dw in registers; a block's groups add theirs in LDS and leave one row of
+// partial sums, which a second launch adds in block order.
 #include "fp8_device.h"
 #include "gate_device.h"
 
@@ -83,7 +83,7 @@ __device__ __forceinline__ float codes8(const float (&y)[8], uint32_t &q0, uint3
     return s;
 }
 
-template <int NV, bool FP8, bool WF32>
+template <int NV, bool FP8, bool WF32, bool STREAM>
 __global__ __launch_bounds__(kWave *kMaxWaves) void norm_kernel(NormArgs a)
 {
     __shared__ float sums[kMaxWaves];
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_kernel(NormArgs a)
                 v[u][i] += r[i];
             const int c = u * threads + tid;
             if (c < nvec)
-                *reinterpret_cast<u32x4 *>(a.res_out + row * a.h + (size_t)c * 8) = narrow8(v[u]);
+                store16_stream(a.res_out + row * a.h + (size_t)c * 8, narrow8(v[u]));
         }
     }
 #pragma unroll
@@ -149,8 +149,13 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_kernel(NormArgs a)
         for (int i = 0; i < 8; ++i)
             y[i] = v[u][i] * inv * w[i];
         const int c = u * threads + tid;
-        if (a.out && c < nvec)
-            *reinterpret_cast<u32x4 *>(a.out + row * a.h + (size_t)c * 8) = narrow8(y);
+        if (a.out && c < nvec) {
+            uint16_t *to = a.out + row * a.h + (size_t)c * 8;
+            if constexpr (STREAM)
+                store16_stream(to, narrow8(y));
+            else
+                *reinterpret_cast<u32x4 *>(to) = narrow8(y);
+        }
         if constexpr (FP8) {
             uint32_t q0, q1;
             const float s = codes8(y, q0, q1);
@@ -170,24 +175,39 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_kernel(NormArgs a)
 }
 
 template <int NV, bool WF32>
-__global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwdArgs a)
+__global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwdArgs a, int waves)
 {
     // the next row's loads go out before this row's sums meet, where the
     // registers hold both rows
     constexpr bool kAhead = NV <= 2;
     __shared__ float2 sums[2][kMaxWaves];
-    const int tid = threadIdx.x, threads = blockDim.x, waves = threads >> 6;
+    extern __shared__ __align__(16) float meet[];  // [groups - 1, h]
+    const int threads = waves * kWave, groups = blockDim.x / threads;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / threads);  // (whole waves)
+    const int tid = threadIdx.x - group * threads;
     const int nvec = a.h >> 3;
     const uint32_t bytes = (uint32_t)nvec * 16u;
     const __amdgpu_buffer_rsrc_t rw = row_rsrc(a.w, (uint32_t)nvec * (WF32 ? 32u : 16u));
-    Weight8<WF32> wv[NV];
+    // held, where the registers allow; else read again where they are used
+    constexpr bool kHold = NV <= 2;
+    Weight8<WF32> wv[kHold ? NV : 1];
+    const auto weight = [&](int u, float (&w)[8]) {
+        if (kHold) {
+            wv[kHold ? u : 0].get(w);
+        } else {
+            Weight8<WF32> v;
+            v.load(rw, (uint32_t)(u * threads + tid));
+            v.get(w);
+        }
+    };
     float dw[NV][8];
     struct Row {
         u32x4 x[NV], d[NV], s[NV];
     } now, next;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-        wv[u].load(rw, (uint32_t)(u * threads + tid));
+        if (kHold)
+            wv[kHold ? u : 0].load(rw, (uint32_t)(u * threads + tid));
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             dw[u][i] = 0.0f;
@@ -207,19 +227,24 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwd
                 r.s[u] = load16_row(rs, (uint32_t)(u * threads + tid) * 16u);
         }
     };
+    const size_t step = (size_t)gridDim.x * groups, last = (size_t)a.T - 1;
+    size_t t = (size_t)blockIdx.x * groups + group;
     int buf = 0;
     if (kAhead)
-        load(next, blockIdx.x);
-    for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x, buf ^= 1) {
+        load(next, min(t, last));
+    // a block's groups make the same number of steps; behind the last row they
+    // read that again and keep nothing
+    for (size_t t0 = (size_t)blockIdx.x * groups; t0 < (size_t)a.T; t0 += step, t += step, buf ^= 1) {
         float ss = 0.0f, sg = 0.0f;
+        const bool live = t <= last;
         if (kAhead)
             now = next;
         else
-            load(now, t);
+            load(now, min(t, last));
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float w[8], v[8], d[8];
-            wv[u].get(w);
+            weight(u, w);
             widen8(now.x[u], v);
             widen8(now.d[u], d);
 #pragma unroll
@@ -227,19 +252,21 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwd
                 ss = __builtin_fmaf(v[i], v[i], ss);
                 sg = __builtin_fmaf(d[i] * w[i], v[i], sg);
             }
+            if (!kAhead)
+                __builtin_amdgcn_sched_barrier(0);  // one vector's values at a time
         }
-        if (kAhead && t + gridDim.x < (size_t)a.T)
-            load(next, t + gridDim.x);
+        if (kAhead && t0 + step < (size_t)a.T)
+            load(next, min(t + step, last));
         ss = wave_sum(ss);
         sg = wave_sum(sg);
         if (waves > 1) {
             // two buffers: a wave that is a row ahead writes the other one
             if (lane_id() == 0)
-                sums[buf][tid >> 6] = float2{ss, sg};
+                sums[buf][threadIdx.x >> 6] = float2{ss, sg};
             __syncthreads();
             ss = sg = 0.0f;
             for (int w = 0; w < waves; ++w) {
-                const float2 p = sums[buf][w];
+                const float2 p = sums[buf][group * waves + w];
                 ss += p.x;
                 sg += p.y;
             }
@@ -252,15 +279,17 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwd
             // would not fit the registers
             opaque(now.x[u]);
             opaque(now.d[u]);
-            opaque(wv[u].lo);
+            if (kHold)
+                opaque(wv[kHold ? u : 0].lo);
             float w[8], v[8], d[8], o[8];
-            wv[u].get(w);
+            weight(u, w);
             widen8(now.x[u], v);
             widen8(now.d[u], d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 o[i] = inv * __builtin_fmaf(-c, v[i], d[i] * w[i]);
-                dw[u][i] = __builtin_fmaf(d[i], v[i] * inv, dw[u][i]);
+                const float s = __builtin_fmaf(d[i], v[i] * inv, dw[u][i]);
+                dw[u][i] = live ? s : dw[u][i];
             }
             if (a.dres) {
                 float s[8];
@@ -270,8 +299,38 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwd
                     o[i] += s[i];
             }
             const int cc = u * threads + tid;
-            if (cc < nvec)
+            if (live && cc < nvec)
                 *reinterpret_cast<u32x4 *>(a.dx + t * a.h + (size_t)cc * 8) = narrow8(o);
+            if (!kAhead)
+                __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if (groups > 1) {
+        if (group > 0) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                const int c = u * threads + tid;
+                if (c < nvec) {
+                    float4 *p = reinterpret_cast<float4 *>(meet + (size_t)(group - 1) * a.h + c * 8);
+                    p[0] = float4{dw[u][0], dw[u][1], dw[u][2], dw[u][3]};
+                    p[1] = float4{dw[u][4], dw[u][5], dw[u][6], dw[u][7]};
+                }
+            }
+        }
+        __syncthreads();
+        if (group > 0)
+            return;
+        for (int g = 0; g < groups - 1; ++g) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                const int c = u * threads + tid;
+                if (c < nvec) {
+                    const float *p = meet + (size_t)g * a.h + c * 8;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dw[u][i] += p[i];
+                }
+            }
         }
     }
     float *part = a.partial + (size_t)blockIdx.x * a.h;
@@ -298,13 +357,22 @@ __global__ __launch_bounds__(256) void norm_weight_kernel(const float *partial, 
     const int c = (blockIdx.x * (256 / kSumLanes) + col) * 4;
     float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < h) {
-#pragma unroll 8
-        for (int r = part; r < rows; r += kSumLanes) {
-            const float4 p = *reinterpret_cast<const float4 *>(partial + (size_t)r * h + c);
-            s.x += p.x;
-            s.y += p.y;
-            s.z += p.z;
-            s.w += p.w;
+        // eight rows' loads at a time, also of the last few (rows behind the
+        // last are read as that and not added)
+        for (int r0 = part; r0 < rows; r0 += 8 * kSumLanes) {
+            float4 p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                p[i] = *reinterpret_cast<const float4 *>(
+                    partial + (size_t)min(r0 + i * kSumLanes, rows - 1) * h + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = r0 + i * kSumLanes < rows;
+                s.x += in ? p[i].x : 0.0f;
+                s.y += in ? p[i].y : 0.0f;
+                s.z += in ? p[i].z : 0.0f;
+                s.w += in ? p[i].w : 0.0f;
+            }
         }
     }
     meet[part][col] = s;
@@ -335,32 +403,76 @@ RowShape row_shape(int h)
     return {nv, (nvec + nv * kWave - 1) / (nv * kWave)};
 }
 
-template <int NV>
-hipError_t launch_norm(const NormArgs &a, bool w_f32, int waves, hipStream_t stream)
+// The normed rows are read next, the sum with the residual only behind the
+// whole layer: it is stored past the caches, and so are normed rows that would
+// not stay in the memory-side cache until they are read. Measured at h = 7168
+// with both and FP8 rows, alone / with a copy of the normed rows behind it, all
+// cached, the sum streamed, both streamed: 1024 rows 14.9 / 20.7, 14.7 / 20.2,
+// 14.7 / 22.4 us; 4096 rows 50.2 / 66.3, 44.3 / 62.2, 46.4 / 68.7; 8192 rows
+// 94 / 145, 93 / 142, 85 / 132.
+constexpr int64_t kStreamBytes = 96ll << 20;
+
+template <int NV, bool FP8, bool WF32>
+void launch_norm(const NormArgs &a, int waves, hipStream_t stream)
 {
     const dim3 grid((unsigned)a.T), block((unsigned)waves * kWave);
-    if (a.codes) {
-        if (w_f32)
-            hipLaunchKernelGGL((norm_kernel<NV, true, true>), grid, block, 0, stream, a);
-        else
-            hipLaunchKernelGGL((norm_kernel<NV, true, false>), grid, block, 0, stream, a);
-    } else if (w_f32) {
-        hipLaunchKernelGGL((norm_kernel<NV, false, true>), grid, block, 0, stream, a);
-    } else {
-        hipLaunchKernelGGL((norm_kernel<NV, false, false>), grid, block, 0, stream, a);
-    }
-    return hipGetLastError();
+    if ((int64_t)a.T * a.h * 2 > kStreamBytes)
+        hipLaunchKernelGGL((norm_kernel<NV, FP8, WF32, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((norm_kernel<NV, FP8, WF32, false>), grid, block, 0, stream, a);
 }
 
 template <int NV>
-hipError_t launch_norm_bwd(const NormBwdArgs &a, bool w_f32, int waves, int blocks,
-                           hipStream_t stream)
+hipError_t launch_norm(const NormArgs &a, bool w_f32, int waves, hipStream_t stream)
 {
-    const dim3 grid((unsigned)blocks), block((unsigned)waves * kWave);
-    if (w_f32)
-        hipLaunchKernelGGL((norm_backward_kernel<NV, true>), grid, block, 0, stream, a);
+    if (a.codes && w_f32)
+        launch_norm<NV, true, true>(a, waves, stream);
+    else if (a.codes)
+        launch_norm<NV, true, false>(a, waves, stream);
+    else if (w_f32)
+        launch_norm<NV, false, true>(a, waves, stream);
     else
-        hipLaunchKernelGGL((norm_backward_kernel<NV, false>), grid, block, 0, stream, a);
+        launch_norm<NV, false, false>(a, waves, stream);
+    return hipGetLastError();
+}
+
+// Blocks and groups of waves of the backward pass. The registers hold 16 waves
+// on a compute unit: two blocks, so that one loads while the other waits for
+// its sums, of up to 8 waves (one block of 14 waves with two rows side by side
+// took 46.5 us for 4096 x 7168 against 42.4). Few narrow rows go side by side
+// in as many blocks as there are compute units, which leaves fewer partial
+// rows to write and add.
+struct BwdShape {
+    RowShape row;
+    int groups, blocks;
+};
+
+constexpr int kBwdUnits = 256;
+
+BwdShape bwd_shape(int T, int h)
+{
+    BwdShape s;
+    s.row = row_shape(h);
+    const int most = s.row.waves < 8 ? 8 / s.row.waves : 1;
+    const int want = (int)(((int64_t)T + kBwdUnits - 1) / kBwdUnits);
+    s.groups = want < 1 ? 1 : want < most ? want : most;
+    const int64_t blocks = ((int64_t)T + s.groups - 1) / s.groups;
+    const int places = kBwdUnits * (s.row.waves <= 8 ? 2 : 1);
+    s.blocks = blocks < places ? (int)blocks : places;
+    return s;
+}
+
+template <int NV>
+hipError_t launch_norm_bwd(const NormBwdArgs &a, bool w_f32, const BwdShape &s, hipStream_t stream)
+{
+    const dim3 grid((unsigned)s.blocks), block((unsigned)(s.row.waves * s.groups) * kWave);
+    const size_t lds = (size_t)(s.groups - 1) * a.h * sizeof(float);
+    if (w_f32)
+        hipLaunchKernelGGL((norm_backward_kernel<NV, true>), grid, block, lds, stream, a,
+                           s.row.waves);
+    else
+        hipLaunchKernelGGL((norm_backward_kernel<NV, false>), grid, block, lds, stream, a,
+                           s.row.waves);
     return hipGetLastError();
 }
 
@@ -375,19 +487,15 @@ hipError_t launch_rms_norm(const NormArgs &a, bool w_f32, hipStream_t stream)
                      : launch_norm<4>(a, w_f32, s.waves, stream);
 }
 
-int norm_bwd_blocks(int T, int h)
-{
-    (void)h;
-    return T < 512 ? T : 512;
-}
+int norm_bwd_blocks(int T, int h) { return bwd_shape(T, h).blocks; }
 
 hipError_t launch_rms_norm_backward(const NormBwdArgs &a, bool w_f32, hipStream_t stream)
 {
-    const int blocks = norm_bwd_blocks(a.T, a.h);
+    const BwdShape s = bwd_shape(a.T, a.h);
+    const int blocks = s.blocks;
     if (blocks > 0) {
-        const RowShape s = row_shape(a.h);
-        const hipError_t e = s.nv == 2 ? launch_norm_bwd<2>(a, w_f32, s.waves, blocks, stream)
-                                       : launch_norm_bwd<4>(a, w_f32, s.waves, blocks, stream);
+        const hipError_t e = s.row.nv == 2 ? launch_norm_bwd<2>(a, w_f32, s, stream)
+                                           : launch_norm_bwd<4>(a, w_f32, s, stream);
         if (e != hipSuccess)
             return e;
     }
