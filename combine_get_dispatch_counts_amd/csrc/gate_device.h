@@ -70,6 +70,16 @@ __device__ __forceinline__ float row_sum(float v)
     return v;
 }
 
+// Over a wave's groups of LANES (16 or 32) adjacent lanes.
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v)
+{
+    v = row_sum(v);
+    if constexpr (LANES == 32)
+        v += __shfl_xor(v, 16, kWave);
+    return v;
+}
+
 // The row's 16 bits of a ballot.
 __device__ __forceinline__ uint32_t row_ballot(bool b)
 {

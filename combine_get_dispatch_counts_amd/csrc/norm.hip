@@ -174,6 +174,58 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_kernel(NormArgs a)
     }
 }
 
+// Rows of at most 8 LANES channels: LANES lanes have a row, a vector each, so a
+// wave has two or four and no block meets. (A wave a row: 32768 x 64 12.6 us,
+// x 256 23.9; this 5.1 and 15.9.)
+constexpr int kNarrowThreads = 256;
+
+template <int LANES, bool FP8, bool WF32>
+__global__ __launch_bounds__(kNarrowThreads) void norm_narrow_kernel(NormArgs a)
+{
+    const int i = threadIdx.x % LANES, nvec = a.h >> 3;
+    const int64_t row = (int64_t)blockIdx.x * (kNarrowThreads / LANES) + threadIdx.x / LANES;
+    const bool live = row < a.T && i < nvec;
+    const size_t at = (size_t)(live ? row * a.h + i * 8 : 0);
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    Weight8<WF32> wv;
+    wv.load(row_rsrc(a.w, (uint32_t)nvec * (WF32 ? 32u : 16u)), (uint32_t)i);
+    float v[8], ss = 0.0f;
+    widen8(live ? load16_stream(a.x + at) : zero, v);
+    if (a.residual) {
+        float r[8];
+        widen8(live ? load16_stream(a.residual + at) : zero, r);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            v[c] += r[c];
+        if (live)
+            store16_stream(a.res_out + at, narrow8(v));
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        ss = __builtin_fmaf(v[c], v[c], ss);
+    ss = group_sum<LANES>(ss);
+    const float inv = 1.0f / __builtin_sqrtf(ss / (float)a.h + a.eps);
+    float w[8], y[8];
+    wv.get(w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        y[c] = v[c] * inv * w[c];
+    if (a.out && live)
+        *reinterpret_cast<u32x4 *>(a.out + at) = narrow8(y);
+    if constexpr (FP8) {
+        uint32_t q0, q1;
+        const float s = codes8(y, q0, q1);
+        if (live)
+            *reinterpret_cast<uint2 *>(a.codes + at) = uint2{q0, q1};
+        // 32 scales a row (128 or 256 channels have one or two groups)
+        const float next = LANES == 32 ? __shfl(s, (lane_id() & 32) + 16, kWave) : 0.0f;
+        if (row < a.T) {
+            for (int g = i; g < 32; g += LANES)
+                a.scales[row * 32 + g] = g == 0 ? s : g == 1 && a.h > 128 ? next : 0.0f;
+        }
+    }
+}
+
 template <int NV, bool WF32>
 __global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwdArgs a, int waves)
 {
@@ -345,6 +397,78 @@ __global__ __launch_bounds__(kWave *kMaxWaves) void norm_backward_kernel(NormBwd
     }
 }
 
+// Rows of at most 8 LANES channels, as the forward pass has them; a wave's
+// groups of lanes walk the rows four steps at a time and meet once at the end.
+constexpr int kNarrowSteps = 4;
+
+template <int LANES, bool WF32>
+__global__ __launch_bounds__(kNarrowThreads) void norm_narrow_backward_kernel(NormBwdArgs a)
+{
+    constexpr int kRows = kNarrowThreads / LANES;
+    __shared__ float meet[kRows][LANES * 8];
+    const int i = threadIdx.x % LANES, mine = threadIdx.x / LANES, nvec = a.h >> 3;
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    Weight8<WF32> wv;
+    wv.load(row_rsrc(a.w, (uint32_t)nvec * (WF32 ? 32u : 16u)), (uint32_t)i);
+    float w[8], dw[8];
+    wv.get(w);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        dw[c] = 0.0f;
+    for (int64_t t0 = (int64_t)blockIdx.x * kRows + mine; t0 - mine < a.T;
+         t0 += kNarrowSteps * step) {
+        u32x4 x[kNarrowSteps], d[kNarrowSteps], s[kNarrowSteps];
+        bool live[kNarrowSteps];
+        size_t at[kNarrowSteps];
+#pragma unroll
+        for (int q = 0; q < kNarrowSteps; ++q) {
+            const int64_t t = t0 + q * step;
+            live[q] = t < a.T && i < nvec;
+            at[q] = (size_t)(live[q] ? t * a.h + i * 8 : 0);
+            x[q] = load16_stream(a.x + at[q]);
+            d[q] = load16_stream(a.dout + at[q]);
+            s[q] = a.dres ? load16_stream(a.dres + at[q]) : zero;
+        }
+#pragma unroll
+        for (int q = 0; q < kNarrowSteps; ++q) {
+            float v[8], g[8], r[8], ss = 0.0f, sg = 0.0f;
+            widen8(live[q] ? x[q] : zero, v);
+            widen8(live[q] ? d[q] : zero, g);
+            widen8(s[q], r);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                ss = __builtin_fmaf(v[c], v[c], ss);
+                sg = __builtin_fmaf(g[c] * w[c], v[c], sg);
+            }
+            ss = group_sum<LANES>(ss);
+            sg = group_sum<LANES>(sg);
+            const float inv = 1.0f / __builtin_sqrtf(ss / (float)a.h + a.eps);
+            const float m = inv * inv * (sg / (float)a.h);
+            float o[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                o[c] = inv * __builtin_fmaf(-m, v[c], g[c] * w[c]) + r[c];
+                const float n = __builtin_fmaf(g[c], v[c] * inv, dw[c]);
+                dw[c] = live[q] ? n : dw[c];  // (a row of zeros without eps is NaN)
+            }
+            if (live[q])
+                *reinterpret_cast<u32x4 *>(a.dx + at[q]) = narrow8(o);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        meet[mine][i * 8 + c] = dw[c];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.h; c += kNarrowThreads) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            sum += meet[r][c];
+        a.partial[(size_t)blockIdx.x * a.h + c] = sum;
+    }
+}
+
 // dw[c] = the sum of the partial rows, in a fixed order: 16 threads have four
 // columns, each a sixteenth of the rows.
 constexpr int kSumLanes = 16;
@@ -422,6 +546,25 @@ void launch_norm(const NormArgs &a, int waves, hipStream_t stream)
         hipLaunchKernelGGL((norm_kernel<NV, FP8, WF32, false>), grid, block, 0, stream, a);
 }
 
+// Widest rows that go to the narrow kernels' 16 and 32 lanes.
+constexpr int kNarrow16 = 128, kNarrow32 = 256;
+
+template <int LANES>
+hipError_t launch_norm_narrow(const NormArgs &a, bool w_f32, hipStream_t stream)
+{
+    constexpr int kRows = kNarrowThreads / LANES;
+    const dim3 grid((unsigned)(((int64_t)a.T + kRows - 1) / kRows)), block(kNarrowThreads);
+    if (a.codes && w_f32)
+        hipLaunchKernelGGL((norm_narrow_kernel<LANES, true, true>), grid, block, 0, stream, a);
+    else if (a.codes)
+        hipLaunchKernelGGL((norm_narrow_kernel<LANES, true, false>), grid, block, 0, stream, a);
+    else if (w_f32)
+        hipLaunchKernelGGL((norm_narrow_kernel<LANES, false, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((norm_narrow_kernel<LANES, false, false>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
 template <int NV>
 hipError_t launch_norm(const NormArgs &a, bool w_f32, int waves, hipStream_t stream)
 {
@@ -476,26 +619,54 @@ hipError_t launch_norm_bwd(const NormBwdArgs &a, bool w_f32, const BwdShape &s, 
     return hipGetLastError();
 }
 
+template <int LANES>
+hipError_t launch_norm_narrow_bwd(const NormBwdArgs &a, bool w_f32, int blocks,
+                                  hipStream_t stream)
+{
+    const dim3 grid((unsigned)blocks), block(kNarrowThreads);
+    if (w_f32)
+        hipLaunchKernelGGL((norm_narrow_backward_kernel<LANES, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((norm_narrow_backward_kernel<LANES, false>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs &a, bool w_f32, hipStream_t stream)
 {
     if (a.T == 0)
         return hipSuccess;
+    if (a.h <= kNarrow32)
+        return a.h <= kNarrow16 ? launch_norm_narrow<16>(a, w_f32, stream)
+                                : launch_norm_narrow<32>(a, w_f32, stream);
     const RowShape s = row_shape(a.h);
     return s.nv == 2 ? launch_norm<2>(a, w_f32, s.waves, stream)
                      : launch_norm<4>(a, w_f32, s.waves, stream);
 }
 
-int norm_bwd_blocks(int T, int h) { return bwd_shape(T, h).blocks; }
+int norm_bwd_blocks(int T, int h)
+{
+    if (h > kNarrow32)
+        return bwd_shape(T, h).blocks;
+    const int rows = kNarrowThreads / (h <= kNarrow16 ? 16 : 32);
+    const int64_t blocks = ((int64_t)T + rows - 1) / rows;
+    return blocks < 2 * kBwdUnits ? (int)blocks : 2 * kBwdUnits;
+}
 
 hipError_t launch_rms_norm_backward(const NormBwdArgs &a, bool w_f32, hipStream_t stream)
 {
-    const BwdShape s = bwd_shape(a.T, a.h);
-    const int blocks = s.blocks;
+    const int blocks = norm_bwd_blocks(a.T, a.h);
     if (blocks > 0) {
-        const hipError_t e = s.row.nv == 2 ? launch_norm_bwd<2>(a, w_f32, s, stream)
-                                           : launch_norm_bwd<4>(a, w_f32, s, stream);
+        hipError_t e;
+        if (a.h <= kNarrow32) {
+            e = a.h <= kNarrow16 ? launch_norm_narrow_bwd<16>(a, w_f32, blocks, stream)
+                                 : launch_norm_narrow_bwd<32>(a, w_f32, blocks, stream);
+        } else {
+            const BwdShape s = bwd_shape(a.T, a.h);
+            e = s.row.nv == 2 ? launch_norm_bwd<2>(a, w_f32, s, stream)
+                              : launch_norm_bwd<4>(a, w_f32, s, stream);
+        }
         if (e != hipSuccess)
             return e;
     }

@@ -91,8 +91,9 @@ def test_norm_fp8(T, h, bf16):
     _norm_case(T, h, bf16, bf16, True, torch.bfloat16 if bf16 else torch.float32)
 
 
-def test_norm_many_rows():
-    _norm_case(2600, 256, True, True, True, torch.bfloat16)
+@pytest.mark.parametrize("h,fp8", [(8, False), (128, True), (136, False), (256, True), (264, False)])
+def test_norm_many_rows(h, fp8):
+    _norm_case(2601, h, True, True, fp8, torch.bfloat16)
 
 
 def test_norm_eps_and_zero_rows():
@@ -147,7 +148,7 @@ def test_norm_in_place():
     same(b, want.residual, "residual")
 
 
-@pytest.mark.parametrize("T,h", NORM_SHAPES + [(1500, 200), (2049, 64)])
+@pytest.mark.parametrize("T,h", NORM_SHAPES + [(1500, 200), (2049, 64), (9001, 128), (4100, 256), (5000, 8), (1300, 264)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm_backward(T, h, residual):
     x, dout = G.rows((T, h), 70), G.rows((T, h), 71, 0.02)
@@ -548,7 +549,7 @@ def test_route_backward_against_differences(scoring):
 
 @pytest.mark.parametrize("T,h,K", [(1, 8, 1), (5, 128, 2), (9, 1032, 3), (4, 2056, 9), (6, 4096, 6),
                                    (5, 4104, 1), (7, 7168, 8), (3, 7176, 32), (2, 16392, 2),
-                                   (130, 256, 8)])
+                                   (130, 256, 8), (33, 136, 3), (17, 264, 5)])
 def test_combine_backward(T, h, K):
     E = max(K, 8)
     idx = _choose(T, E, K, 140, 0.15 if T > 2 else 0.0)
