@@ -549,7 +549,7 @@ def test_route_backward_against_differences(scoring):
 
 @pytest.mark.parametrize("T,h,K", [(1, 8, 1), (5, 128, 2), (9, 1032, 3), (4, 2056, 9), (6, 4096, 6),
                                    (5, 4104, 1), (7, 7168, 8), (3, 7176, 32), (2, 16392, 2),
-                                   (130, 256, 8), (33, 136, 3), (17, 264, 5)])
+                                   (130, 256, 8), (33, 136, 3), (17, 264, 5), (900, 4096, 8)])
 def test_combine_backward(T, h, K):
     E = max(K, 8)
     idx = _choose(T, E, K, 140, 0.15 if T > 2 else 0.0)
