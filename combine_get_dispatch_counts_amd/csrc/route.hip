@@ -772,9 +772,9 @@ __global__ __launch_bounds__(kWave, N <= 16 ? 4 : 2) void route_kernel(RouteArgs
 // their rows; the last block to end adds the losses. A batch of one run needs
 // the first launch alone.
 
-template <int N>
+template <int N, int TOKENS>
 struct Run {
-    static constexpr int kTokensOfRun = N == 32 ? 32 : 64;
+    static constexpr int kTokensOfRun = TOKENS;
     static constexpr int kWaves = kTokensOfRun / kTokens;
     static constexpr int kColumns = kRow * N;
     static constexpr int kThreads = kWaves * kWave;
@@ -784,7 +784,7 @@ struct Run {
     static constexpr int kShare = kTokensOfRun / kShares;
 };
 
-constexpr int kFinalColumns = 64, kFinalThreads = 256;
+constexpr int kFinalColumns = 64, kFinalThreads = 1024;
 
 struct BalanceWs {
     unsigned int *done;  // blocks of the second launch that have ended
@@ -796,11 +796,18 @@ struct BalanceWs {
 
 __host__ __device__ inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-__host__ __device__ inline int run_tokens(int E) { return E > 256 ? 32 : 64; }
+// Tokens of a run: 64, or with more than 128 experts 32, so that two blocks
+// share a compute unit (65536 tokens of 256 experts 29.6 us against 38.5, 1024
+// 9.9 against 11.9) -- but 64 still where that spares the second launch (64
+// tokens 6.6 against 9.2; above 256 experts the LDS does not hold them).
+__host__ __device__ inline int run_tokens(int T, int E)
+{
+    return E <= 128 || (E <= 256 && T <= 64) ? 64 : 32;
+}
 
 __host__ __device__ inline int64_t balance_rows(int T, int E, int S)
 {
-    return ((int64_t)T + run_tokens(E) - 1) / run_tokens(E) + (int64_t)S;
+    return ((int64_t)T + run_tokens(T, E) - 1) / run_tokens(T, E) + (int64_t)S;
 }
 
 __host__ __device__ inline BalanceWs balance_ws(void *ws, int T, int E, int S)
@@ -859,10 +866,10 @@ __device__ __forceinline__ int sequence_of(const int32_t *off, int S, int t)
     return lo <= S ? lo - 1 : -1;
 }
 
-template <int N, bool SIGMOID>
-__global__ __launch_bounds__(Run<N>::kThreads) void balance_kernel(BalanceArgs a, bool wide)
+template <int N, int TOKENS, bool SIGMOID>
+__global__ __launch_bounds__((Run<N, TOKENS>::kThreads)) void balance_kernel(BalanceArgs a, bool wide)
 {
-    typedef Run<N> R;
+    typedef Run<N, TOKENS> R;
     __shared__ __align__(16) float share[R::kTokensOfRun][R::kColumns];
     __shared__ __align__(16) uint32_t cnt[R::kTokensOfRun][R::kColumns / 2];  // two experts a word
     __shared__ int seq[R::kTokensOfRun];
@@ -1036,15 +1043,18 @@ __device__ __forceinline__ int tokens_seen(const BalanceWs &ws, int s, int r0, i
 
 __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArgs a, int parts)
 {
-    constexpr int kShares = kFinalThreads / kFinalColumns;  // waves: they share the rows
+    constexpr int kShares = kFinalThreads / kFinalColumns;  // of the rows
+    constexpr int kWaves = kFinalThreads / kWave;
     __shared__ float sum_p[kShares][kFinalColumns];
     __shared__ int sum_c[kShares][kFinalColumns];
-    __shared__ float total_w[kShares];
-    __shared__ int some_w[kShares];
+    __shared__ float total_w[kWaves];
+    __shared__ int some_w[kWaves];
     __shared__ bool last;
     const int s = blockIdx.x / parts, part = blockIdx.x - s * parts, tid = threadIdx.x;
-    const int wave = tid / kWave, lane = lane_id(), e = part * kFinalColumns + lane;
-    const int per = run_tokens(a.E);
+    const int wave = tid / kWave, lane = lane_id();
+    const int col = tid % kFinalColumns, share = tid / kFinalColumns;
+    const int e = part * kFinalColumns + col;
+    const int per = run_tokens(a.T, a.E);
     const BalanceWs ws = balance_ws(a.ws, a.T, a.E, a.S);
     int lo, hi;
     bool bad = false;
@@ -1053,26 +1063,43 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
     float q = 0.0f;
     int c = 0;
     if (e < a.E) {
-#pragma unroll 8
-        for (int r = r0 + wave; r < r1; r += kShares) {
-            q += ws.probs[(size_t)(r + s) * a.E + e];
-            c += ws.counts[(size_t)(r + s) * a.E + e];
+        // eight rows' loads at a time (rows behind the last are read as that
+        // and not added)
+        for (int r = r0 + share; r < r1; r += 8 * kShares) {
+            float p[8];
+            int n[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const size_t at = (size_t)(min(r + i * kShares, r1 - 1) + s) * a.E + e;
+                p[i] = ws.probs[at];
+                n[i] = ws.counts[at];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = r + i * kShares < r1;
+                q += in ? p[i] : 0.0f;
+                c += in ? n[i] : 0;
+            }
         }
     }
-    const int n = tokens_seen(ws, s, r0, r1);
-    sum_p[wave][lane] = q;
-    sum_c[wave][lane] = c;
+    sum_p[share][col] = q;
+    sum_c[share][col] = c;
+    const int n = wave == 0 ? tokens_seen(ws, s, r0, r1) : 0;
     __syncthreads();
     if (wave == 0) {
+        q = 0.0f;
+        c = 0;
+        if (lane < kFinalColumns) {
 #pragma unroll
-        for (int w = 1; w < kShares; ++w) {
-            q += sum_p[w][lane];
-            c += sum_c[w][lane];
-        }
-        q = n ? q / (float)n : 0.0f;
-        if (e < a.E) {
-            a.counts[(size_t)s * a.E + e] = c;
-            a.probs[(size_t)s * a.E + e] = q;
+            for (int i = 0; i < kShares; ++i) {
+                q += sum_p[i][lane];
+                c += sum_c[i][lane];
+            }
+            q = n ? q / (float)n : 0.0f;
+            if (e < a.E) {
+                a.counts[(size_t)s * a.E + e] = c;
+                a.probs[(size_t)s * a.E + e] = q;
+            }
         }
         const float dot = wave_sum((float)c * q);
         if (lane == 0) {
@@ -1113,7 +1140,7 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
     if (tid == 0) {
         total = 0.0f;
         some = 0;
-        for (int w = 0; w < kShares; ++w) {
+        for (int w = 0; w < kWaves; ++w) {
             total += total_w[w];
             some += some_w[w];
         }
@@ -1336,17 +1363,17 @@ hipError_t route_for(const RouteArgs &a, bool sigmoid, bool normalize, hipStream
                     : route_for<N, EPX_MAX_TOPK>(a, sigmoid, normalize, stream);
 }
 
-template <int N>
+template <int N, int TOKENS>
 hipError_t balance_for(const BalanceArgs &a, bool sigmoid, hipStream_t stream)
 {
-    typedef Run<N> R;
+    typedef Run<N, TOKENS> R;
     const int runs = a.T > 0 ? (int)(((int64_t)a.T + R::kTokensOfRun - 1) / R::kTokensOfRun) : 1;
     const dim3 grid((unsigned)runs), block(R::kThreads);
     const bool wide = wide_rows(a.logits, a.E);
     if (sigmoid)
-        hipLaunchKernelGGL((balance_kernel<N, true>), grid, block, 0, stream, a, wide);
+        hipLaunchKernelGGL((balance_kernel<N, TOKENS, true>), grid, block, 0, stream, a, wide);
     else
-        hipLaunchKernelGGL((balance_kernel<N, false>), grid, block, 0, stream, a, wide);
+        hipLaunchKernelGGL((balance_kernel<N, TOKENS, false>), grid, block, 0, stream, a, wide);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || runs == 1)
         return e;
@@ -1397,7 +1424,7 @@ hipError_t launch_route(const RouteArgs &a, bool sigmoid, bool normalize, hipStr
 
 size_t balance_workspace_bytes(int T, int E, int S)
 {
-    if (T <= run_tokens(E))  // one run: the first launch alone
+    if (T <= run_tokens(T, E))  // one run: the first launch alone
         return 0;
     const size_t rows = (size_t)balance_rows(T, E, S);
     const size_t parts = (E + kFinalColumns - 1) / kFinalColumns;
@@ -1407,12 +1434,13 @@ size_t balance_workspace_bytes(int T, int E, int S)
 hipError_t launch_balance(const BalanceArgs &a, bool sigmoid, hipStream_t stream)
 {
     if (a.E <= 64)
-        return balance_for<4>(a, sigmoid, stream);
+        return balance_for<4, 64>(a, sigmoid, stream);
     if (a.E <= 128)
-        return balance_for<8>(a, sigmoid, stream);
+        return balance_for<8, 64>(a, sigmoid, stream);
     if (a.E <= 256)
-        return balance_for<16>(a, sigmoid, stream);
-    return balance_for<32>(a, sigmoid, stream);
+        return run_tokens(a.T, a.E) == 64 ? balance_for<16, 64>(a, sigmoid, stream)
+                                          : balance_for<16, 32>(a, sigmoid, stream);
+    return balance_for<32, 32>(a, sigmoid, stream);
 }
 
 hipError_t launch_route_backward(const RouteBwdArgs &a, bool sigmoid, bool normalize,

@@ -152,8 +152,9 @@ def balance(l, idx, scoring, off=None):
             losses.append(float((counts[s].double() * probs[s]).sum()) * E / (K * n))
         seen.append(n)
     loss = sum(losses) / len(losses) if losses else 0.0
-    # a wave adds a run's tokens, a block its waves, the last launch the runs
-    adds = 64 + 16 + -(-T // 64) + 16
+    # a block adds a run's tokens (64 at most), the last launch the runs (of 32
+    # tokens at least), in any order
+    adds = 64 + -(-T // 32)
     rel = (adds + 2 * (4 + float(spread(l).max() if T else 0.0)) + 14 + 6) * U
     return loss, counts, probs, torch.tensor(seen + [len(losses)], dtype=torch.int32), rel
 
