@@ -964,7 +964,7 @@ int epx_balance_loss(epx_ctx *ctx, const float *logits, const int64_t *topk_idx,
     a.logits = logits; a.topk_idx = topk_idx; a.seq_off = seq_off;
     a.T = T; a.E = E; a.K = K; a.S = S;
     a.loss = loss; a.counts = counts; a.probs = probs; a.num_tokens = num_tokens;
-    a.ws = ws; a.err = ctx->d_err;
+    a.ws_base = ws; a.err = ctx->d_err;
     return launched(epx::launch_balance(a, scoring == EPX_SIGMOID, stream));
 }
 

@@ -53,6 +53,15 @@ struct RouteArgs {
 
 hipError_t launch_route(const RouteArgs &a, bool sigmoid, bool normalize, hipStream_t stream);
 
+// The balance loss's workspace.
+struct BalanceWs {
+    unsigned int *done;  // blocks of the second launch that have ended
+    float *dot;          // [S, ceil(E / 64)]: sums of counts * probs
+    int *seen;           // [rows]
+    int *counts;         // [rows, E]
+    float *probs;        // [rows, E]
+};
+
 struct BalanceArgs {
     const float *logits;      // [T, E]
     const int64_t *topk_idx;  // [T, K]
@@ -62,7 +71,8 @@ struct BalanceArgs {
     int32_t *counts;          // [S, E]
     float *probs;             // [S, E]
     int32_t *num_tokens;      // [S + 1]
-    void *ws;
+    void *ws_base;            // workspace
+    BalanceWs ws;             // its parts (set by the launcher)
     int *err;
 };
 

@@ -786,46 +786,41 @@ struct Run {
 
 constexpr int kFinalColumns = 64, kFinalThreads = 1024;
 
-struct BalanceWs {
-    unsigned int *done;  // blocks of the second launch that have ended
-    float *dot;          // [S, ceil(E / 64)]: sums of counts * probs
-    int *seen;           // [rows]
-    int *counts;         // [rows, E]
-    float *probs;        // [rows, E]
-};
-
-__host__ __device__ inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
+inline size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // Tokens of a run: 64, or with more than 128 experts 32, so that two blocks
 // share a compute unit (65536 tokens of 256 experts 29.6 us against 38.5, 1024
 // 9.9 against 11.9) -- but 64 still where that spares the second launch (64
 // tokens 6.6 against 9.2; above 256 experts the LDS does not hold them).
-__host__ __device__ inline int run_tokens(int T, int E)
+__host__ __device__ inline int run_shift(int T, int E)
 {
-    return E <= 128 || (E <= 256 && T <= 64) ? 64 : 32;
+    return E <= 128 || (E <= 256 && T <= 64) ? 6 : 5;
 }
 
-__host__ __device__ inline int64_t balance_rows(int T, int E, int S)
+inline int run_tokens(int T, int E) { return 1 << run_shift(T, E); }
+
+inline int64_t balance_rows(int T, int E, int S)
 {
     return ((int64_t)T + run_tokens(T, E) - 1) / run_tokens(T, E) + (int64_t)S;
 }
 
-__host__ __device__ inline BalanceWs balance_ws(void *ws, int T, int E, int S)
+// The parts of a workspace that begins at p; returns its bytes.
+size_t balance_ws(char *p, int T, int E, int S, BalanceWs &w)
 {
-    const int64_t rows = balance_rows(T, E, S);
+    const size_t rows = (size_t)balance_rows(T, E, S);
     const size_t parts = (E + kFinalColumns - 1) / kFinalColumns;
-    char *p = static_cast<char *>(ws);
-    BalanceWs w;
+    char *const p0 = p;
     w.done = reinterpret_cast<unsigned int *>(p);
     p += 16;
     w.dot = reinterpret_cast<float *>(p);
     p += up16((size_t)S * parts * 4);
     w.seen = reinterpret_cast<int *>(p);
-    p += up16((size_t)rows * 4);
+    p += up16(rows * 4);
     w.counts = reinterpret_cast<int *>(p);
-    p += up16((size_t)rows * E * 4);
+    p += up16(rows * E * 4);
     w.probs = reinterpret_cast<float *>(p);
-    return w;
+    p += up16(rows * E * 4);
+    return (size_t)(p - p0);
 }
 
 // Sequence s's tokens, kept inside [0, T).
@@ -877,7 +872,7 @@ __global__ __launch_bounds__((Run<N, TOKENS>::kThreads)) void balance_kernel(Bal
     __shared__ float seq_loss[R::kTokensOfRun];
     const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
     const int mine = tid / kRow, i = row_lane();  // this token of the run
-    const BalanceWs ws = balance_ws(a.ws, a.T, a.E, a.S);
+    const BalanceWs &ws = a.ws;
     const bool whole = gridDim.x == 1;
     const int64_t t = (int64_t)blockIdx.x * R::kTokensOfRun + mine;
     bool bad_off = false, bad_logit = false, bad_route = false;
@@ -1054,12 +1049,12 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
     const int wave = tid / kWave, lane = lane_id();
     const int col = tid % kFinalColumns, share = tid / kFinalColumns;
     const int e = part * kFinalColumns + col;
-    const int per = run_tokens(a.T, a.E);
-    const BalanceWs ws = balance_ws(a.ws, a.T, a.E, a.S);
+    const int shift = run_shift(a.T, a.E);
+    const BalanceWs &ws = a.ws;
     int lo, hi;
     bool bad = false;
     sequence(a.seq_off, s, a.T, lo, hi, bad);
-    const int r0 = hi > lo ? lo / per : 0, r1 = hi > lo ? (hi - 1) / per + 1 : 0;
+    const int r0 = hi > lo ? lo >> shift : 0, r1 = hi > lo ? ((hi - 1) >> shift) + 1 : 0;
     float q = 0.0f;
     int c = 0;
     if (e < a.E) {
@@ -1426,13 +1421,14 @@ size_t balance_workspace_bytes(int T, int E, int S)
 {
     if (T <= run_tokens(T, E))  // one run: the first launch alone
         return 0;
-    const size_t rows = (size_t)balance_rows(T, E, S);
-    const size_t parts = (E + kFinalColumns - 1) / kFinalColumns;
-    return 16 + up16((size_t)S * parts * 4) + up16(rows * 4) + 2 * up16(rows * E * 4);
+    BalanceWs w;
+    return balance_ws(nullptr, T, E, S, w);
 }
 
-hipError_t launch_balance(const BalanceArgs &a, bool sigmoid, hipStream_t stream)
+hipError_t launch_balance(const BalanceArgs &args, bool sigmoid, hipStream_t stream)
 {
+    BalanceArgs a = args;
+    balance_ws(static_cast<char *>(a.ws_base), a.T, a.E, a.S, a.ws);
     if (a.E <= 64)
         return balance_for<4, 64>(a, sigmoid, stream);
     if (a.E <= 128)
