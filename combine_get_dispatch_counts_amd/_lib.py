@@ -15,7 +15,7 @@ DEV_BAD_ROUTE, DEV_OVERFLOW, DEV_BAD_HANDLE, DEV_WORKSPACE, DEV_BAD_LOGIT = 1, 2
 MAX_TOPK, MAX_EXPERTS, MAX_RANKS, MAX_SWEEP_GBPS = 32, 512, 64, 100000
 NOALLOC_SCRATCH_BYTES = 1 << 20
 MAX_CHANNELS, MAX_DECODE_TOKENS, MAX_EXPERT_BYTES = 65536, 64, 0xFFFF0000
-MAX_NORM_CHANNELS = 32768
+MAX_NORM_CHANNELS, MAX_ROUTER_TOKENS, MAX_SEQUENCES = 32768, 1 << 27, 1 << 24
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int

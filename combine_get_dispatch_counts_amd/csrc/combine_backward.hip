@@ -163,10 +163,8 @@ hipError_t launch(const CombineBwdArgs &a, hipStream_t stream)
 
 }  // namespace
 
-hipError_t launch_combine_backward(const CombineBwdArgs &a, hipStream_t stream)
+static hipError_t launch_tokens(const CombineBwdArgs &a, hipStream_t stream)
 {
-    if (a.T == 0)
-        return hipSuccess;
     if (a.h <= 128)
         return launch_narrow<16>(a, stream);
     if (a.h <= 256)
@@ -178,6 +176,26 @@ hipError_t launch_combine_backward(const CombineBwdArgs &a, hipStream_t stream)
     if (a.h <= 4096)
         return launch<8>(a, stream);
     return launch<14>(a, stream);
+}
+
+hipError_t launch_combine_backward(const CombineBwdArgs &args, hipStream_t stream)
+{
+    // a launch has at most 2^31 threads (8 waves a token, or 32 lanes an entry
+    // of up to 32): more tokens go in several
+    const int64_t most = 1ll << 21;
+    CombineBwdArgs a = args;
+    for (int64_t t = 0; t < args.T; t += most) {
+        a.T = (int)(args.T - t < most ? args.T - t : most);
+        const hipError_t e = launch_tokens(a, stream);
+        if (e != hipSuccess)
+            return e;
+        a.dout += most * a.h;
+        a.topk_w += most * a.K;
+        a.pos += most * a.K;
+        if (a.dtopk_w)
+            a.dtopk_w += most * a.K;
+    }
+    return hipSuccess;
 }
 
 }  // namespace epx

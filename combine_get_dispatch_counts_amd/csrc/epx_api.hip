@@ -854,7 +854,8 @@ int epx_rms_norm(epx_ctx *ctx, const uint16_t *x, const uint16_t *residual, cons
         return rc;
     if (T > 0) {
         if (!x || !weight || (!out && !codes) || (codes && !scales) || (scales && !codes) ||
-            (residual && !residual_out) || (residual_out && !residual))
+            (residual && !residual_out) || (residual_out && !residual) ||
+            (out && out == residual_out))
             return EPX_EINVAL;
         if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) ||
             !aligned16(residual_out) || !aligned16(out) || !aligned16(codes) ||
@@ -905,7 +906,7 @@ int epx_rms_norm_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *x,
 // the choice itself.
 static int check_router(int T, int K, int E, int scoring)
 {
-    if (scoring != EPX_SOFTMAX && scoring != EPX_SIGMOID)
+    if ((scoring != EPX_SOFTMAX && scoring != EPX_SIGMOID) || T > EPX_MAX_ROUTER_TOKENS)
         return EPX_EINVAL;
     return check_routing(T, K, E, 1);
 }
@@ -937,7 +938,7 @@ int epx_route(epx_ctx *ctx, const float *logits, const float *bias, const uint8_
 
 size_t epx_balance_workspace(int T, int E, int S)
 {
-    if (check_routing(T, 1, E, 1) != EPX_OK || S < 1)
+    if (check_router(T, 1, E, EPX_SOFTMAX) != EPX_OK || S < 1 || S > EPX_MAX_SEQUENCES)
         return 0;
     return epx::balance_workspace_bytes(T, E, S);
 }
@@ -952,7 +953,7 @@ int epx_balance_loss(epx_ctx *ctx, const float *logits, const int64_t *topk_idx,
         return rc;
     if ((rc = check_router(T, K, E, scoring)) != EPX_OK)
         return rc;
-    if (S < 1 || (!seq_off && S != 1) || !loss || !counts || !probs || !num_tokens ||
+    if (S < 1 || S > EPX_MAX_SEQUENCES || (!seq_off && S != 1) || !loss || !counts || !probs || !num_tokens ||
         !aligned16(ws) || (T > 0 && (!logits || !topk_idx)))
         return EPX_EINVAL;
     const size_t need = epx_balance_workspace(T, E, S);
@@ -979,7 +980,7 @@ int epx_route_backward(epx_ctx *ctx, const float *logits, const int64_t *topk_id
     if ((rc = check_router(T, K, E, scoring)) != EPX_OK)
         return rc;
     if (!(scale > -3.0e38f && scale < 3.0e38f) || (!dtopk_w && !counts) ||
-        (counts ? !num_tokens || !dloss || S < 1 || (!seq_off && S != 1)
+        (counts ? !num_tokens || !dloss || S < 1 || S > EPX_MAX_SEQUENCES || (!seq_off && S != 1)
                 : num_tokens || dloss || seq_off))
         return EPX_EINVAL;
     if (T > 0 && (!logits || !topk_idx || !dlogits))

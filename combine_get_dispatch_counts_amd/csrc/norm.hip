@@ -633,16 +633,38 @@ hipError_t launch_norm_narrow_bwd(const NormBwdArgs &a, bool w_f32, int blocks,
 
 }  // namespace
 
-hipError_t launch_rms_norm(const NormArgs &a, bool w_f32, hipStream_t stream)
+hipError_t launch_rms_norm(const NormArgs &args, bool w_f32, hipStream_t stream)
 {
-    if (a.T == 0)
-        return hipSuccess;
-    if (a.h <= kNarrow32)
-        return a.h <= kNarrow16 ? launch_norm_narrow<16>(a, w_f32, stream)
-                                : launch_norm_narrow<32>(a, w_f32, stream);
-    const RowShape s = row_shape(a.h);
-    return s.nv == 2 ? launch_norm<2>(a, w_f32, s.waves, stream)
-                     : launch_norm<4>(a, w_f32, s.waves, stream);
+    // a launch has at most 2^31 threads: more rows go in several
+    const RowShape s = row_shape(args.h);
+    const int per_row = args.h <= kNarrow16 ? 16 : args.h <= kNarrow32 ? 32 : s.waves * kWave;
+    const int64_t most = (1ll << 31) / per_row;
+    NormArgs a = args;
+    for (int64_t row = 0; row < args.T; row += most) {
+        a.T = (int)(args.T - row < most ? args.T - row : most);
+        hipError_t e;
+        if (a.h <= kNarrow32)
+            e = a.h <= kNarrow16 ? launch_norm_narrow<16>(a, w_f32, stream)
+                                 : launch_norm_narrow<32>(a, w_f32, stream);
+        else
+            e = s.nv == 2 ? launch_norm<2>(a, w_f32, s.waves, stream)
+                          : launch_norm<4>(a, w_f32, s.waves, stream);
+        if (e != hipSuccess)
+            return e;
+        const int64_t step = most * a.h;
+        a.x += step;
+        if (a.residual) {
+            a.residual += step;
+            a.res_out += step;
+        }
+        if (a.out)
+            a.out += step;
+        if (a.codes) {
+            a.codes += step;
+            a.scales += most * scale_stride(a.h);
+        }
+    }
+    return hipSuccess;
 }
 
 int norm_bwd_blocks(int T, int h)

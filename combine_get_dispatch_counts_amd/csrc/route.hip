@@ -1045,72 +1045,78 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
     __shared__ float total_w[kWaves];
     __shared__ int some_w[kWaves];
     __shared__ bool last;
-    const int s = blockIdx.x / parts, part = blockIdx.x - s * parts, tid = threadIdx.x;
-    const int wave = tid / kWave, lane = lane_id();
+    const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
     const int col = tid % kFinalColumns, share = tid / kFinalColumns;
-    const int e = part * kFinalColumns + col;
     const int shift = run_shift(a.T, a.E);
     const BalanceWs &ws = a.ws;
-    int lo, hi;
-    bool bad = false;
-    sequence(a.seq_off, s, a.T, lo, hi, bad);
-    const int r0 = hi > lo ? lo >> shift : 0, r1 = hi > lo ? ((hi - 1) >> shift) + 1 : 0;
-    float q = 0.0f;
-    int c = 0;
-    if (e < a.E) {
-        // eight rows' loads at a time (rows behind the last are read as that
-        // and not added)
-        for (int r = r0 + share; r < r1; r += 8 * kShares) {
-            float p[8];
-            int n[8];
+    // 64 experts of a sequence, and with more sequences than blocks others behind
+    for (uint32_t item = blockIdx.x; item < (uint32_t)(a.S * parts); item += gridDim.x) {
+        const int s = (int)(item / (uint32_t)parts), part = (int)item - s * parts;
+        const int e = part * kFinalColumns + col;
+        int lo, hi;
+        bool bad = false;
+        sequence(a.seq_off, s, a.T, lo, hi, bad);
+        const int r0 = hi > lo ? lo >> shift : 0, r1 = hi > lo ? ((hi - 1) >> shift) + 1 : 0;
+        float q = 0.0f;
+        int c = 0;
+        if (e < a.E) {
+            // eight rows' loads at a time (rows behind the last are read as that
+            // and not added)
+            for (int r = r0 + share; r < r1; r += 8 * kShares) {
+                float p[8];
+                int n[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const size_t at = (size_t)(min(r + i * kShares, r1 - 1) + s) * a.E + e;
-                p[i] = ws.probs[at];
-                n[i] = ws.counts[at];
-            }
+                for (int i = 0; i < 8; ++i) {
+                    const size_t at = (size_t)(min(r + i * kShares, r1 - 1) + s) * a.E + e;
+                    p[i] = ws.probs[at];
+                    n[i] = ws.counts[at];
+                }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool in = r + i * kShares < r1;
-                q += in ? p[i] : 0.0f;
-                c += in ? n[i] : 0;
+                for (int i = 0; i < 8; ++i) {
+                    const bool in = r + i * kShares < r1;
+                    q += in ? p[i] : 0.0f;
+                    c += in ? n[i] : 0;
+                }
             }
         }
+        sum_p[share][col] = q;
+        sum_c[share][col] = c;
+        const int n = wave == 0 ? tokens_seen(ws, s, r0, r1) : 0;
+        __syncthreads();
+        if (wave == 0) {
+            q = 0.0f;
+            c = 0;
+            if (lane < kFinalColumns) {
+#pragma unroll
+                for (int i = 0; i < kShares; ++i) {
+                    q += sum_p[i][lane];
+                    c += sum_c[i][lane];
+                }
+                q = n ? q / (float)n : 0.0f;
+                if (e < a.E) {
+                    a.counts[(size_t)s * a.E + e] = c;
+                    a.probs[(size_t)s * a.E + e] = q;
+                }
+            }
+            const float dot = wave_sum((float)c * q);
+            if (lane == 0) {
+                if (part == 0)
+                    a.num_tokens[s] = n;
+                // -1 marks a sequence without tokens (the sums are not negative)
+                __hip_atomic_store(&ws.dot[item],
+                                   n ? dot * ((float)a.E / ((float)a.K * (float)n)) : -1.0f,
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        __syncthreads();
     }
-    sum_p[share][col] = q;
-    sum_c[share][col] = c;
-    const int n = wave == 0 ? tokens_seen(ws, s, r0, r1) : 0;
-    __syncthreads();
-    if (wave == 0) {
-        q = 0.0f;
-        c = 0;
-        if (lane < kFinalColumns) {
-#pragma unroll
-            for (int i = 0; i < kShares; ++i) {
-                q += sum_p[i][lane];
-                c += sum_c[i][lane];
-            }
-            q = n ? q / (float)n : 0.0f;
-            if (e < a.E) {
-                a.counts[(size_t)s * a.E + e] = c;
-                a.probs[(size_t)s * a.E + e] = q;
-            }
-        }
-        const float dot = wave_sum((float)c * q);
-        if (lane == 0) {
-            if (part == 0)
-                a.num_tokens[s] = n;
-            // -1 marks a sequence without tokens (the sums are not negative)
-            __hip_atomic_store(&ws.dot[blockIdx.x],
-                               n ? dot * ((float)a.E / ((float)a.K * (float)n)) : -1.0f,
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            // the sum has left this XCD's L2 (a device-coherent store, waited for)
-            // before the block counts itself; nothing else is handed over, so
-            // the L2 need not be written back
-            __builtin_amdgcn_s_waitcnt(0);
-            last = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_RELAXED,
-                                          __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-        }
+    if (tid == 0) {
+        // the sums have left this XCD's L2 (device-coherent stores, waited for)
+        // before the block counts itself; nothing else is handed over, so the
+        // L2 need not be written back
+        __builtin_amdgcn_s_waitcnt(0);
+        last = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               gridDim.x - 1;
     }
     __syncthreads();
     if (!last)
@@ -1120,7 +1126,7 @@ __global__ __launch_bounds__(kFinalThreads) void balance_final_kernel(BalanceArg
     for (int q = tid; q < a.S; q += kFinalThreads) {
         float v = 0.0f;
         for (int p = 0; p < parts; ++p)
-            v += __hip_atomic_load(&ws.dot[q * parts + p], __ATOMIC_RELAXED,
+            v += __hip_atomic_load(&ws.dot[(size_t)q * parts + p], __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
         total += v >= 0.0f ? v : 0.0f;
         some += v >= 0.0f;
@@ -1373,9 +1379,7 @@ hipError_t balance_for(const BalanceArgs &a, bool sigmoid, hipStream_t stream)
     if (e != hipSuccess || runs == 1)
         return e;
     const int parts = (a.E + kFinalColumns - 1) / kFinalColumns;
-    const int64_t blocks = (int64_t)a.S * parts;
-    if (blocks > 0x7FFFFFFF)
-        return hipErrorInvalidValue;
+    const int64_t items = (int64_t)a.S * parts, blocks = items < (1 << 16) ? items : 1 << 16;
     hipLaunchKernelGGL(balance_final_kernel, dim3((unsigned)blocks), dim3(kFinalThreads), 0,
                        stream, a, parts);
     return hipGetLastError();

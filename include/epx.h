@@ -71,6 +71,8 @@ extern "C" {
 #define EPX_MAX_SWEEP_GBPS 100000
 #define EPX_MAX_CHANNELS 65536      /* K, N and f of the experts' products */
 #define EPX_MAX_NORM_CHANNELS 32768 /* h of the norm */
+#define EPX_MAX_ROUTER_TOKENS (1 << 27) /* T of the router's calls */
+#define EPX_MAX_SEQUENCES (1 << 24) /* S of the balance loss */
 #define EPX_MAX_DECODE_TOKENS 64    /* T of epx_moe_decode */
 #define EPX_MAX_EXPERT_BYTES 0xFFFF0000ll /* one expert's matrix (w13: both halves) */
 #define EPX_NOALLOC_SCRATCH_BYTES (1u << 20) /* see epx_get_dispatch_layout_noalloc */
@@ -552,8 +554,8 @@ int epx_moe_decode(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_i
  *      from the rounded v, nor the codes from the rounded y.
  * h a multiple of 8, with codes of 128 (else EPX_EUNSUPPORTED), at most
  * EPX_MAX_NORM_CHANNELS. Buffers 16-byte aligned. residual_out may be residual or
- * x, and out may be x or residual where it is not residual_out too; no other
- * overlap. The squares are summed in fp32: rows with values beyond 1e18 / h
+ * x, and out may be x or residual where it is not residual_out too (EPX_EINVAL);
+ * no other overlap. The squares are summed in fp32: rows with values beyond 1e18 / h
  * leave its range. A row with an Inf or NaN gives NaN. */
 int epx_rms_norm(epx_ctx *ctx, const uint16_t *x, const uint16_t *residual, const void *weight,
                  int weight_fp32, int T, int h, float eps, uint16_t *residual_out, uint16_t *out,
@@ -602,8 +604,8 @@ int epx_rms_norm_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *x,
  *      epx_moe_decode and epx_combine read them.
  * Scores are in fp32 with full relative precision down to their underflow;
  * normalized weights also below it. The choice is that of the exact scores of
- * the given logits, computed again in 64 bits where fp32 cannot tell. K <= E
- * and K <= EPX_MAX_TOPK; rows of no token are not read. */
+ * the given logits, computed again in 64 bits where fp32 cannot tell. K <= E,
+ * K <= EPX_MAX_TOPK, E <= EPX_MAX_EXPERTS, T <= EPX_MAX_ROUTER_TOKENS. */
 int epx_route(epx_ctx *ctx, const float *logits, const float *bias, const uint8_t *mask, int T,
               int E, int K, int scoring, int num_groups, int topk_groups, int normalize,
               float scale, int64_t *topk_idx, float *topk_w, hipStream_t stream);
@@ -622,7 +624,7 @@ size_t epx_balance_workspace(int T, int E, int S);
  *      route; others outside [0, E) set EPX_DEV_BAD_ROUTE and are skipped; an
  *      expert named twice counts twice); seq_off [S+1] int32, sequence s being
  *      tokens [seq_off[s], seq_off[s+1]), or NULL: one sequence of all T
- *      (S = 1). Tokens of no sequence do not count. Offsets that decrease or
+ *      (S = 1; at most EPX_MAX_SEQUENCES). Tokens of no sequence do not count. Offsets that decrease or
  *      leave [0, T] set EPX_DEV_OVERFLOW. ws: epx_balance_workspace bytes
  *      (may be NULL if that is 0), 16-byte aligned, no initial contents; calls
  *      that share it must not overlap.

@@ -169,6 +169,30 @@ def test_norm_backward(T, h, residual):
     X.assert_close(dw[:h], ref_w, tol_w, "dweight")
 
 
+@pytest.mark.parametrize("h,T", [(8, (1 << 27) + 5), (264, (1 << 25) + 3)])
+def test_norm_more_rows_than_a_launch(h, T):
+    """Rows beyond the 2^31 threads of one launch, and offsets beyond 2^32 bytes."""
+    base = G.rows((1 << 12, h), 79)
+    say(f"rms_norm T={T} h={h}")
+    x = torch.empty((T, h), dtype=torch.bfloat16, device=DEV)
+    x[:1 << 12] = gpu(base)
+    done = 1 << 12
+    while done < T:                            # the same rows again and again
+        n = min(done, T - done)
+        x[done:done + n] = x[:n]
+        done += n
+    b = epx().rms_norm(x, torch.ones(h, device=DEV))
+    torch.cuda.synchronize()
+    flags()
+    y, inv = G.norm(base.double(), torch.ones(h).double(), 1e-6)
+    tol = G.norm_tol(y, base.double(), inv, torch.ones(h).double())
+    for r in (0, (1 << 31) // (16 if h == 8 else 64) - 2, T - 3, 1 << 24):
+        at = torch.arange(r, min(r + 3, T)) % (1 << 12)
+        X.assert_close(b.out[r:r + 3], y[at], tol[at] + G.BF16 * (y[at].abs() + tol[at]), f"row {r}")
+    del x, b
+    torch.cuda.empty_cache()
+
+
 def test_norm_backward_in_place_and_empty():
     x, dout, dres, w = gpu(G.rows((9, 264), 74), G.rows((9, 264), 75), G.rows((9, 264), 76),
                            torch.ones(264))
@@ -213,7 +237,7 @@ def _route(l, K, scoring="softmax", bias=None, G_=1, top=1, normalize=True, scal
 
 @pytest.mark.parametrize("E,K", [(1, 1), (2, 2), (7, 3), (8, 2), (63, 6), (64, 8), (65, 5),
                                  (100, 32), (128, 1), (160, 6), (255, 8), (256, 8), (257, 16),
-                                 (384, 8), (512, 10)])
+                                 (384, 8), (512, 10), (512, 32), (300, 31), (32, 32)])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_route(E, K, scoring, normalize):
@@ -225,7 +249,8 @@ def test_route(E, K, scoring, normalize):
 @pytest.mark.parametrize("E,G_,top,K", [(8, 2, 1, 3), (8, 8, 3, 3), (64, 8, 3, 6), (72, 8, 2, 9),
                                         (96, 3, 2, 8), (160, 8, 3, 6), (256, 8, 4, 8),
                                         (256, 64, 5, 8), (256, 4, 4, 8), (320, 5, 1, 32),
-                                        (512, 16, 4, 8)])
+                                        (512, 16, 4, 8), (512, 32, 7, 20), (64, 8, 1, 10),
+                                        (100, 50, 20, 30), (12, 3, 1, 4), (512, 2, 1, 16)])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 def test_route_groups(E, G_, top, K, scoring, biased):
@@ -368,6 +393,36 @@ def _balance(l, idx, scoring, off=None, bits=(), ref_off=None):
                                    (200, 128, 32), (300, 160, 6), (513, 256, 8), (130, 512, 10)])
 def test_balance(T, E, K, scoring):
     _balance(_logits(T, E, 100 + E), _choose(T, E, K, 101), scoring)
+
+
+@pytest.mark.parametrize("T,S", [(70, 70000), (20000, 9000)])
+def test_balance_many_sequences(T, S):
+    """More sequences than tokens or blocks, most of them empty."""
+    g = G.gen(109)
+    cuts = torch.sort(torch.randint(0, T + 1, (S - 1,), generator=g)).values
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), cuts, torch.tensor([T])])
+    l, idx = _logits(T, 16, 108), _choose(T, 16, 2, 107)
+    say(f"balance_loss T={T} S={S}")
+    b = epx().balance_loss(gpu(l), gpu(idx), "softmax", gpu(off.to(torch.int32)))
+    flags()
+    seq = torch.searchsorted(off, torch.arange(T), right=True) - 1
+    p, seen = torch.softmax(l.double(), 1), (idx >= 0).any(1)
+    n = torch.zeros(S, dtype=torch.int64).index_add_(0, seq, seen.long())
+    counts = torch.zeros((S, 17), dtype=torch.int64)
+    counts.index_put_((seq[:, None].expand_as(idx), torch.where(idx >= 0, idx, 16)),
+                      torch.ones_like(idx), accumulate=True)
+    probs = torch.zeros((S, 16), dtype=torch.float64).index_add_(0, seq[seen], p[seen])
+    probs = probs / n.clamp(min=1)[:, None]
+    assert torch.equal(b.counts.cpu().long(), counts[:, :16])
+    assert torch.equal(b.num_tokens.cpu().long(), torch.cat([n, (n > 0).sum().view(1)]))
+    # a sequence has few tokens here: the scores' own errors and some 20 additions
+    rel = (2 * (4 + float(G.spread(l).max())) + 14 + 6 + 64) * G.U
+    X.assert_close(b.probs, probs, rel * probs + G.TINY, "probs")
+    each = (counts[:, :16] * probs).sum(1) * 16 / (2 * n.clamp(min=1))
+    loss = each[n > 0].mean()
+    # the losses of S sequences in a thread's turn, a block's threads, its waves
+    X.assert_close(b.loss, loss.view(1), ((rel + (S / 1024 + 64) * G.U) * loss + G.TINY).view(1),
+                   "loss")
 
 
 SEQUENCES = {
@@ -738,7 +793,7 @@ def test_binding_refuses():
     l, idx = gpu(_logits(4, 16, 171)), torch.zeros((4, 2), dtype=torch.int64, device=DEV)
     top, pos = torch.zeros((4, 2), device=DEV), torch.zeros((4, 2), dtype=torch.int32, device=DEV)
     b = m.balance_loss(l, idx)
-    one = torch.ones(1, device=DEV)
+    one, b16 = torch.ones(1, device=DEV), x.clone()
     off = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
     for err, call in [
         (TypeError, lambda: m.rms_norm(x.float(), w)),
@@ -751,6 +806,7 @@ def test_binding_refuses():
         (ValueError, lambda: m.rms_norm(x, w, residual=x, buf=m.Normed(out=x.clone()))),
         (ValueError, lambda: m.rms_norm(x, w, buf=m.Normed(out=x.clone(), residual=x.clone()))),
         (ValueError, lambda: m.rms_norm(x, w, buf=m.Normed(out=x.clone(), scales=w))),
+        (m.EpxError, lambda: m.rms_norm(x, w, residual=x, buf=m.Normed(out=b16, residual=b16))),
         (ValueError, lambda: m.rms_norm(x, w.cpu())),
         (ValueError, lambda: m.rms_norm_backward(x[:3], x, w)),
         (ValueError, lambda: m.rms_norm_backward(x, x, w, dresidual=x[:1])),
