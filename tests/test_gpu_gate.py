@@ -631,6 +631,26 @@ def test_combine_backward(T, h, K):
     same(b, dw[:T], "d_topk_weights alone")
 
 
+@pytest.mark.parametrize("T,h,K", [((1 << 21) + 5, 8, 2), ((1 << 21) + 3, 264, 1)])
+def test_combine_backward_more_tokens_than_a_launch(T, h, K):
+    g = torch.Generator(device="cuda").manual_seed(148)
+    n = T * K
+    pos = torch.randperm(n, generator=g, device=DEV).to(torch.int32).view(T, K)
+    w = torch.rand((T, K), generator=g, device=DEV)
+    dout = torch.randn((T, h), generator=g, device=DEV).bfloat16()
+    y = torch.randn((n, h), generator=g, device=DEV).bfloat16()
+    say(f"combine_backward T={T} h={h} K={K}")
+    dy, dw = epx().combine_backward(dout, y, pos, w)
+    flags()
+    for k in range(K):
+        for t in torch.arange(T, device=DEV).split(1 << 20):
+            r = pos[t, k].long()
+            same(dy[r], (w[t, k][:, None] * dout[t].float()).to(torch.bfloat16), "d_expert_out")
+            x = dout[t].double() * y[r].double()
+            tol = (h / 64 + 14) * G.U * x.abs().sum(1)
+            assert bool(((dw[t, k].double() - x.sum(1)).abs() <= tol).all())
+
+
 def test_combine_backward_bad_handle():
     dout, y, w = gpu(G.rows((3, 64), 144), G.rows((4, 64), 145), torch.rand((3, 2)))
     pos = torch.tensor([[0, 4], [-7, 1], [3, 2]], dtype=torch.int32)
