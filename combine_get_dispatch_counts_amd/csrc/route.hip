@@ -46,13 +46,11 @@ __device__ __forceinline__ void load_row(const V *row, int E, bool wide, V (&v)[
     }
 }
 
-// A token's logits: -inf where the lane has no expert or the token is not
-// live, and for a NaN or +inf, which sets bad.
+// A token's logits as loaded: -inf where the lane has no expert or the token is
+// not live, and for a NaN or +inf, which sets bad.
 template <int N>
-__device__ __forceinline__ void load_logits(const float *row, int E, bool wide, bool live,
-                                            float (&l)[N], bool &bad)
+__device__ __forceinline__ void clean_logits(int E, bool live, float (&l)[N], bool &bad)
 {
-    load_row<N, float4, float>(row, E, wide, l);
     const int end = live ? E : 0;
     if (__ballot(end != kRow * N)) {
 #pragma unroll
@@ -501,9 +499,12 @@ __global__ __launch_bounds__(kWave, N <= 16 ? 4 : 2) void route_kernel(RouteArgs
     const int64_t tc = min(t, (int64_t)a.T - 1);  // what is read in place of a token behind the last
     const bool live = t < a.T && (!a.mask || a.mask[tc]);
     const float *logits = a.logits + (size_t)tc * a.E;
-    float l[N];
+    float l[N], b[N];
     bool bad = false;
-    load_logits<N>(logits, a.E, wide, live, l, bad);
+    load_row<N, float4, float>(logits, a.E, wide, l);
+    if (a.bias)
+        load_row<N, float4, float>(a.bias, a.E, wide_bias, b);
+    clean_logits<N>(a.E, live, l, bad);
     const float top_l = largest(l);
     float sum_l = 1.0f;  // of the softmax, where the weights need it
     if (!SIGMOID && !normalize) {
@@ -547,8 +548,7 @@ __global__ __launch_bounds__(kWave, N <= 16 ? 4 : 2) void route_kernel(RouteArgs
         }
         if (a.bias) {
             bool odd = false;
-            float b[N], m = 0.0f;
-            load_row<N, float4, float>(a.bias, a.E, wide_bias, b);
+            float m = 0.0f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 key[j] += b[j];
@@ -838,28 +838,47 @@ __device__ __forceinline__ void sequence(const int32_t *off, int s, int T, int &
     bad |= a != lo || b != hi;
 }
 
-// The sequence that token t is in, or -1: the offsets that are not above t are
-// the first ones, and the last of them begins it. The token's 16 lanes look at
-// 64 offsets at a time, so that up to 63 sequences take one load's latency.
-__device__ __forceinline__ int sequence_of(const int32_t *off, int S, int t)
-{
-    if (!off)
-        return 0;
-    int lo = 0, n = S + 1;  // offsets [lo, lo + n) are not decided
-    while (__ballot(n > 0)) {
-        const int step = (n + 63) >> 6;
-        int c = 0;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int at = (m * kRow + row_lane() + 1) * step - 1;
-            const int o = off[min(lo + at, S)];
-            c += __builtin_popcount(row_ballot(n > 0 && at < n && o <= t));
-        }
-        lo += c * step;
-        n = n > 0 ? min(n - c * step, step - 1) : 0;
+// The sequence that a token is in: the offsets that are not above t are the
+// first ones, and the last of them begins it. The token's 16 lanes look at 64
+// offsets at a time, so that up to 63 sequences take one load's latency; that
+// load is apart, to go out before the token's own.
+struct SequenceSearch {
+    int o[4];
+    static __device__ __forceinline__ int step(int n) { return (n + 63) >> 6; }
+    static __device__ __forceinline__ int at(int m, int n)
+    {
+        return (m * kRow + row_lane() + 1) * step(n) - 1;
     }
-    return lo <= S ? lo - 1 : -1;
-}
+    __device__ __forceinline__ void load(const int32_t *off, int S, int lo, int n)
+    {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            o[m] = off[min(lo + at(m, n), S)];
+    }
+    __device__ __forceinline__ void begin(const int32_t *off, int S)
+    {
+        if (off)
+            load(off, S, 0, S + 1);
+    }
+    // the number, or -1
+    __device__ __forceinline__ int find(const int32_t *off, int S, int t)
+    {
+        if (!off)
+            return 0;
+        int lo = 0, n = S + 1;  // offsets [lo, lo + n) are not decided
+        for (;;) {
+            int c = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                c += __builtin_popcount(row_ballot(n > 0 && at(m, n) < n && o[m] <= t));
+            lo += c * step(n);
+            n = n > 0 ? min(n - c * step(n), step(n) - 1) : 0;
+            if (!__ballot(n > 0))
+                return lo <= S ? lo - 1 : -1;
+            load(off, S, lo, n);
+        }
+    }
+};
 
 template <int N, int TOKENS, bool SIGMOID>
 __global__ __launch_bounds__((Run<N, TOKENS>::kThreads)) void balance_kernel(BalanceArgs a, bool wide)
@@ -878,6 +897,8 @@ __global__ __launch_bounds__((Run<N, TOKENS>::kThreads)) void balance_kernel(Bal
     bool bad_off = false, bad_logit = false, bad_route = false;
 
     // what is read of the token, before its sequence is known
+    SequenceSearch search;
+    search.begin(a.seq_off, a.S);
     constexpr int kPer = 2;  // entries of a lane: i, i + 16
     int64_t e[kPer];
 #pragma unroll
@@ -890,11 +911,10 @@ __global__ __launch_bounds__((Run<N, TOKENS>::kThreads)) void balance_kernel(Bal
     for (int j = 0; j < N; ++j)
         l[j] = -kInf;
     if (a.T > 0)
-        load_logits<N>(a.logits + (size_t)min(t, (int64_t)a.T - 1) * a.E, a.E, wide, t < a.T, l,
-                       bad_logit);
+        load_row<N, float4, float>(a.logits + (size_t)min(t, (int64_t)a.T - 1) * a.E, a.E, wide, l);
     for (int c = tid; c < R::kTokensOfRun * R::kColumns / 8; c += R::kThreads)
         reinterpret_cast<uint4 *>(&cnt[0][0])[c] = uint4{0u, 0u, 0u, 0u};
-    int s = sequence_of(a.seq_off, a.S, (int)min(t, (int64_t)a.T));
+    int s = search.find(a.seq_off, a.S, (int)min(t, (int64_t)a.T));
     s = t < a.T ? s : -1;
     bool named[kPer];
 #pragma unroll
@@ -903,6 +923,7 @@ __global__ __launch_bounds__((Run<N, TOKENS>::kThreads)) void balance_kernel(Bal
         bad_route |= s >= 0 && (e[m] < -1 || e[m] >= a.E);
     }
     const bool seen = row_ballot(named[0] || named[1]) != 0;
+    clean_logits<N>(a.E, t < a.T, l, bad_logit);
     bad_logit = bad_logit && seen;
     if (i == 0) {
         seq[mine] = s;
@@ -1172,20 +1193,40 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
     const int row = lane_id() / kRow, i = row_lane();
     const int64_t t = (int64_t)blockIdx.x * kTokens + row;
     const bool live = t < a.T;
+    const int64_t tc = min(t, (int64_t)a.T - 1);  // what is read in place of a token behind the last
     bool bad = false, bad_route = false;
+    // loads in the order of their use: loads end in the order of their issue
+    SequenceSearch search;
+    if (a.counts)
+        search.begin(a.seq_off, a.S);
+    int64_t v[kPer];
+    float d[kPer], l[N];
+#pragma unroll
+    for (int m = 0; m < kPer; ++m)
+        v[m] = a.topk_idx[tc * a.K + min(i + m * kRow, a.K - 1)];
+#pragma unroll
+    for (int m = 0; m < kPer; ++m)
+        d[m] = a.dtopk_w ? a.dtopk_w[tc * a.K + min(i + m * kRow, a.K - 1)] : 0.0f;
+    load_row<N, float4, float>(a.logits + (size_t)tc * a.E, a.E, wide, l);
+    const int s = a.counts ? search.find(a.seq_off, a.S, (int)min(t, (int64_t)a.T)) : -1;
+    int cnt[N];  // (of experts that there are; the others have no share)
+    float tokens = 0.0f, sequences = 1.0f, dloss = 0.0f;
+    if (a.counts) {
+        load_row<N, int4, int>(a.counts + (size_t)max(s, 0) * a.E, a.E, wide_counts, cnt);
+        tokens = (float)a.num_tokens[max(s, 0)];
+        sequences = (float)a.num_tokens[a.S];
+        dloss = a.dloss[0];
+    }
     int e[kPer];
-    float d[kPer];
+    float lk[kPer];
 #pragma unroll
     for (int m = 0; m < kPer; ++m) {
-        const int k = i + m * kRow;
-        const int64_t v = live && k < a.K ? a.topk_idx[t * a.K + k] : -1;
-        d[m] = live && k < a.K && a.dtopk_w ? a.dtopk_w[t * a.K + k] : 0.0f;
-        bad_route |= v < -1 || v >= a.E;
-        e[m] = v >= 0 && v < a.E ? (int)v : -1;
+        v[m] = live && i + m * kRow < a.K ? v[m] : -1;
+        bad_route |= v[m] < -1 || v[m] >= a.E;
+        e[m] = v[m] >= 0 && v[m] < a.E ? (int)v[m] : -1;
+        lk[m] = a.dtopk_w ? a.logits[(size_t)tc * a.E + max(e[m], 0)] : 0.0f;
     }
-    float l[N];
-    const int64_t tc = min(t, (int64_t)a.T - 1);  // what is read in place of a token behind the last
-    load_logits<N>(a.logits + (size_t)tc * a.E, a.E, wide, live, l, bad);
+    clean_logits<N>(a.E, live, l, bad);
     const bool routed = row_ballot(e[0] >= 0 || (kPer > 1 && e[kPer - 1] >= 0)) != 0;
     bad = bad && routed;
     // the gradients with respect to shares (D) and logits (dl)
@@ -1195,18 +1236,14 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
         D[j] = dl[j] = 0.0f;
     bool shares = a.dtopk_w && !normalize && !SIGMOID;
     if (a.counts) {
-        const int s = sequence_of(a.seq_off, a.S, (int)min(t, (int64_t)a.T));
         if (s >= 0 && routed) {
-            const float n = (float)a.num_tokens[s];
-            const float c = n > 0.0f ? a.dloss[0] * ((float)a.E / (float)a.K) /
-                                           (float)max(a.num_tokens[a.S], 1) / (n * n)
-                                     : 0.0f;
-            int cnt[N];  // (of experts that there are; the others have no share)
-            load_row<N, int4, int>(a.counts + (size_t)s * a.E, a.E, wide_counts, cnt);
+            const float c = tokens > 0.0f ? dloss * ((float)a.E / (float)a.K) /
+                                                fmaxf(sequences, 1.0f) / (tokens * tokens)
+                                          : 0.0f;
             // what all shares' gradients have in common is none of the logits',
             // as the shares sum to one: counts relative to an even spread, so
             // that nearly equal ones do not cancel in fp32
-            const float even = n * (float)a.K / (float)a.E;
+            const float even = tokens * (float)a.K / (float)a.E;
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 D[j] = c * ((float)cnt[j] - even);
@@ -1214,11 +1251,10 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
         shares = true;
     }
     if (a.dtopk_w) {
-        float g[kPer], lk[kPer];
+        float g[kPer];
 #pragma unroll
         for (int m = 0; m < kPer; ++m) {
-            lk[m] = e[m] >= 0 ? a.logits[(size_t)tc * a.E + e[m]] : -kInf;
-            lk[m] = lk[m] < kInf ? lk[m] : -kInf;
+            lk[m] = e[m] >= 0 && lk[m] < kInf ? lk[m] : -kInf;
             d[m] = e[m] >= 0 ? d[m] * a.scale : 0.0f;
         }
         if (normalize) {
