@@ -110,14 +110,21 @@ __device__ __forceinline__ void widen8(const u32x4 &p, float (&f)[8])
     }
 }
 
+// Two fp32 values rounded to bf16, nearest even, by gfx950's convert (a fifth of
+// f32_to_bf16's instructions; a NaN stays one, not the canonical one).
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi)
+{
+    return __builtin_bit_cast(uint32_t,
+                              __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
+}
+
 __device__ __forceinline__ u32x4 narrow8(const float (&f)[8])
 {
-    u32x4 o;
-    o.x = f32_to_bf16(f[0]) | (f32_to_bf16(f[1]) << 16);
-    o.y = f32_to_bf16(f[2]) | (f32_to_bf16(f[3]) << 16);
-    o.z = f32_to_bf16(f[4]) | (f32_to_bf16(f[5]) << 16);
-    o.w = f32_to_bf16(f[6]) | (f32_to_bf16(f[7]) << 16);
-    return o;
+    return u32x4{narrow2(f[0], f[1]), narrow2(f[2], f[3]), narrow2(f[4], f[5]),
+                 narrow2(f[6], f[7])};
 }
 
 }  // namespace epx

@@ -138,6 +138,21 @@ def test_norm_non_finite_rows():
     flags()
 
 
+def test_norm_residual_rounds_everywhere():
+    """Sums of every pair of exponents, denormal ones too, rounded nearest even."""
+    bits = torch.randint(0, 1 << 16, (2, 64, 4096), generator=G.gen(64)).to(torch.int16)
+    x, r = bits.view(torch.bfloat16)
+    x, r = (torch.where(t.isfinite(), t, torch.zeros_like(t)) for t in (x, r))
+    # neighbours in size, so that both count: r's exponent within 10 of x's
+    e = ((x.view(torch.int16).int() >> 7) & 0xFF) + torch.randint(-10, 11, x.shape, generator=G.gen(65))
+    near = (r.view(torch.int16).int() & 0x807F) | (e.clamp(0, 254) << 7)
+    r[::2] = near.to(torch.int16).view(torch.bfloat16)[::2]
+    b = epx().rms_norm(gpu(x), torch.ones(4096, device=DEV), residual=gpu(r))
+    same(b.residual.cpu(), (x.float() + r.float()).to(torch.bfloat16), "residual")
+    assert (b.residual.float().abs() < 1e-38).any() and (b.residual != 0).any()
+    flags()
+
+
 def test_norm_in_place():
     """The sum over the residual, the normed rows over x."""
     x, r, w = gpu(G.rows((33, 1416), 62), G.rows((33, 1416), 63), torch.ones(1416))
