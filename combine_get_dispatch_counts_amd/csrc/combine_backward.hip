@@ -6,7 +6,9 @@
 // holds the token's row in registers (its other waves find it in the cache),
 // reads the entry's expert row once, stores the scaled row and sums the
 // products over the wave. HBM-bound: per entry one row read and one written
-// (4096 tokens of top-8 x 7168, 1 GB: 170-178 us, 5.7 TB/s).
+// (4096 tokens of top-8 x 7168, 1 GB: 170-174 us, 5.8 TB/s). Few tokens are
+// bound by the wave that has an entry, its loads and then its stores: 16 tokens
+// 7.4 us, 128 10.3, 512 25.1 (5.0 TB/s).
 #include "gate_device.h"
 
 namespace epx {
@@ -80,7 +82,7 @@ __global__ __launch_bounds__(kWave * 8) void combine_backward_kernel(CombineBwdA
 }
 
 // Rows of at most 8 LANES channels: LANES lanes have an entry, a vector each, so
-// a wave has two or four. (32768 tokens of top-8 x 128: 27.5 us, 5.2 TB/s; a
+// a wave has two or four. (32768 tokens of top-8 x 128: 26.1 us, 5.5 TB/s; a
 // wave an entry 83.7.)
 constexpr int kNarrowThreads = 256;
 
@@ -132,7 +134,7 @@ hipError_t launch_narrow(const CombineBwdArgs &a, hipStream_t stream)
 // With many rows the sums and the scaled rows take a launch each: the token's
 // row is read twice, but memory reads alone and then writes alone. One against
 // two launches, top-8, h = 7168: 256 tokens (28 MB of expert rows) 12.4 / 13.3
-// us, 512 25.6 / 24.5, 1024 51 / 46.5, 4096 194 / 170-178, 8192 385 / 337; h =
+// us, 512 25.6 / 24.5, 1024 51 / 46.5, 4096 194 / 170-174, 8192 385 / 337; h =
 // 2048, 4096 tokens 57 / 52; top-6 x 4096, 4096 tokens 80 / 74.5. Where the
 // token's row is a larger part, or rows are short, one launch: 8192 tokens of
 // top-2 x 4096 55 / 64, of top-4 x 2048 51 / 53, of top-8 x 1024 52 / 56. (Rows

@@ -953,8 +953,8 @@ int epx_balance_loss(epx_ctx *ctx, const float *logits, const int64_t *topk_idx,
         return rc;
     if ((rc = check_router(T, K, E, scoring)) != EPX_OK)
         return rc;
-    if (S < 1 || S > EPX_MAX_SEQUENCES || (!seq_off && S != 1) || !loss || !counts || !probs || !num_tokens ||
-        !aligned16(ws) || (T > 0 && (!logits || !topk_idx)))
+    if (S < 1 || S > EPX_MAX_SEQUENCES || (!seq_off && S != 1) || !loss || !counts || !probs ||
+        !num_tokens || !aligned16(ws) || (T > 0 && (!logits || !topk_idx)))
         return EPX_EINVAL;
     const size_t need = epx_balance_workspace(T, E, S);
     if (need > 0 && !ws)

@@ -555,8 +555,10 @@ int epx_moe_decode(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_i
  * h a multiple of 8, with codes of 128 (else EPX_EUNSUPPORTED), at most
  * EPX_MAX_NORM_CHANNELS. Buffers 16-byte aligned. residual_out may be residual or
  * x, and out may be x or residual where it is not residual_out too (EPX_EINVAL);
- * no other overlap. The squares are summed in fp32: rows with values beyond 1e18 / h
- * leave its range. A row with an Inf or NaN gives NaN. */
+ * no other overlap. The squares are summed in fp32: rows with values beyond
+ * 1e18 / h leave its range, and where eps is as small as they are rows of
+ * values below 1e-18 do (with eps = 0 a row of zeros gives NaN). A row with an
+ * Inf or NaN gives NaN. */
 int epx_rms_norm(epx_ctx *ctx, const uint16_t *x, const uint16_t *residual, const void *weight,
                  int weight_fp32, int T, int h, float eps, uint16_t *residual_out, uint16_t *out,
                  uint8_t *codes, float *scales, hipStream_t stream);
@@ -624,8 +626,9 @@ size_t epx_balance_workspace(int T, int E, int S);
  *      route; others outside [0, E) set EPX_DEV_BAD_ROUTE and are skipped; an
  *      expert named twice counts twice); seq_off [S+1] int32, sequence s being
  *      tokens [seq_off[s], seq_off[s+1]), or NULL: one sequence of all T
- *      (S = 1; at most EPX_MAX_SEQUENCES). Tokens of no sequence do not count. Offsets that decrease or
- *      leave [0, T] set EPX_DEV_OVERFLOW. ws: epx_balance_workspace bytes
+ *      (S = 1; at most EPX_MAX_SEQUENCES). Tokens of no sequence do not count.
+ *      Offsets that decrease or leave [0, T] set EPX_DEV_OVERFLOW, and the
+ *      outputs then say nothing. ws: epx_balance_workspace bytes
  *      (may be NULL if that is 0), 16-byte aligned, no initial contents; calls
  *      that share it must not overlap.
  * Out: loss [1] fp32; counts [S, E] int32 (c_e); probs [S, E] fp32 (P_e);
@@ -646,7 +649,7 @@ int epx_balance_loss(epx_ctx *ctx, const float *logits, const int64_t *topk_idx,
  *      counts, num_tokens as epx_balance_loss left them, seq_off and S as
  *      given to it, and dloss [1] fp32 (device), the gradient of the loss; or
  *      all NULL (S is then not looked at). At least one of dtopk_w and counts.
- * Out: dlogits [T, E] fp32, written whole. */
+ * Out: dlogits [T, E] fp32, written whole; no overlap with the inputs. */
 int epx_route_backward(epx_ctx *ctx, const float *logits, const int64_t *topk_idx, int T, int E,
                        int K, int scoring, int normalize, float scale, const float *dtopk_w,
                        const int32_t *counts, const int32_t *num_tokens, const float *dloss,
