@@ -175,7 +175,7 @@ __device__ __forceinline__ void shares_of(const float (&l)[N], float (&p)[N], fl
 // Bound by vector instructions, not by memory: 16384 tokens of 256 experts, top-8
 // of the best 4 of 8 groups, sigmoid with a bias (18 MB, 2.6 us at a read's
 // rate) 15.6 us at 1080 instructions a wave, four waves a SIMD. Without the
-// second look it would be 12.4: some 30 tokens take it, and a path that few
+// second look it would be 12.4: some ten tokens take it, and a path that few
 // waves run waits for its own instructions as for its data. Softmax without
 // groups or bias 8.4 us. 128 tokens 3.1: one wave's chain of a load, the merges
 // and the weights.

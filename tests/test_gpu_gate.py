@@ -794,6 +794,93 @@ def test_step_is_repeatable_and_replays():
             same(a, b, f"replay {replay}")
 
 
+def _repeated(base, T):
+    """T rows: those of base again and again."""
+    out = torch.empty((T, base.shape[1]), dtype=base.dtype, device=DEV)
+    out[:len(base)] = gpu(base)
+    done = len(base)
+    while done < T:
+        n = min(done, T - done)
+        out[done:done + n] = out[:n]
+        done += n
+    return out
+
+
+def test_router_beyond_32_bit_offsets():
+    """More than 2^31 logits: a token's results do not depend on where it is."""
+    T, E, K, B = (1 << 23) + 5, 264, 3, 4096
+    base = gpu(_logits(B, E, 170))
+    l = _repeated(base, T)
+    say(f"route, balance_loss, route_backward T={T} E={E}")
+    bi, bw = epx().route(base, K)
+    idx, w = epx().route(l, K)
+    d = torch.randn((B, K), generator=G.gen(171)).to(DEV)
+    dd = _repeated(d, T)
+    bl = epx().route_backward(base, bi, dtopk_weights=d)
+    dl = epx().route_backward(l, idx, dtopk_weights=dd)
+    b = epx().balance_loss(l, idx)
+    flags()
+    for r in (0, (1 << 31) // E // B * B, T // B * B):
+        n = min(B, T - r)
+        same(idx[r:r + n], bi[:n], f"topk_idx from {r}")
+        same(w[r:r + n], bw[:n], f"topk_w from {r}")
+        same(dl[r:r + n], bl[:n], f"dlogits from {r}")
+    counts = torch.bincount(bi.flatten(), minlength=E) * (T // B)
+    counts += torch.bincount(bi[:T % B].flatten(), minlength=E)
+    assert torch.equal(b.counts[0].long(), counts) and b.num_tokens.tolist() == [T, 1]
+    del l, idx, w, dl, dd
+    torch.cuda.empty_cache()
+
+
+def test_norm_backward_beyond_32_bit_offsets():
+    T, h, B = (1 << 18) + 5, 8200, 512
+    base, dbase = G.rows((B, h), 172), G.rows((B, h), 173)
+    w = torch.ones(h, device=DEV)
+    say(f"rms_norm_backward T={T} h={h}")
+    want, _ = epx().rms_norm_backward(gpu(dbase), gpu(base), w)
+    x, dout = _repeated(base, T), _repeated(dbase, T)
+    dx, dw = epx().rms_norm_backward(dout, x, w)
+    flags()
+    for r in (0, (1 << 31) // h // B * B, T // B * B):
+        n = min(B, T - r)
+        same(dx[r:r + n], want[:n], f"dx from {r}")
+    v = base.double()
+    term = dbase.double() * v * (v.square().mean(1, keepdim=True) + 1e-6) ** -0.5
+    times = torch.full((B, 1), T // B).double()
+    times[:T % B] += 1
+    # a thread adds a row after the other, T / 256 of them or fewer, then come the
+    # groups, the blocks and the error of a row's own sum (below 200 in all)
+    tol = (T / 256 + 200) * G.U * (times * term.abs()).sum(0)
+    X.assert_close(dw, (times * term).sum(0), tol, "dweight")
+    del x, dout, dx
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,h,K", [((1 << 16) + 1, 4104, 8), (300001, 7168, 1)])
+def test_combine_backward_beyond_32_bit_offsets(T, h, K):
+    """More than 2^31 elements of expert rows, in one launch and in two."""
+    n = T * K
+    g = torch.Generator(device="cuda").manual_seed(174)
+    pos = torch.randperm(n, generator=g, device=DEV).to(torch.int32).view(T, K)
+    w = torch.rand((T, K), generator=g, device=DEV)
+    dout = torch.randn((T, h), generator=g, device=DEV).bfloat16()
+    y = _repeated(torch.randn((1024, h), generator=G.gen(175)).bfloat16(), n)
+    say(f"combine_backward T={T} h={h} K={K}")
+    dy, dw = epx().combine_backward(dout, y, pos, w)
+    flags()
+    inverse = torch.empty(n, dtype=torch.int64, device=DEV)
+    inverse[pos.flatten().long()] = torch.arange(n, device=DEV)
+    for r in (0, (1 << 31) // h - 1000, n - 2000):
+        tk = inverse[r:r + 2000]
+        d = dout[tk // K]
+        same(dy[r:r + 2000], (w.flatten()[tk][:, None] * d.float()).to(torch.bfloat16), f"rows from {r}")
+        x = d.double() * y[r:r + 2000].double()
+        tol = (h / 64 + 14) * G.U * x.abs().sum(1)
+        assert bool(((dw.flatten()[tk].double() - x.sum(1)).abs() <= tol).all())
+    del dout, y, dy
+    torch.cuda.empty_cache()
+
+
 def test_two_streams_at_once():
     """Calls that overlap on two streams, each with its own workspace."""
     l = [gpu(_logits(3000, 64, 160 + i)) for i in range(2)]
