@@ -806,6 +806,32 @@ def _repeated(base, T):
     return out
 
 
+def test_router_takes_rows_off_16_bytes():
+    """Tensors that start 4 bytes behind a 16-byte boundary give the same bytes."""
+    def off(t):
+        flat = torch.empty(t.numel() + 4, dtype=t.dtype, device=DEV)
+        view = flat[1:1 + t.numel()].view(t.shape)
+        view.copy_(t)
+        assert view.data_ptr() % 16 != 0
+        return view
+
+    T, E, K = 70, 64, 6
+    l, bias = gpu(_logits(T, E, 176)), gpu(_logits(1, E, 177, 0.1)[0])
+    say("router's calls on unaligned tensors")
+    idx, w = epx().route(l, K, "sigmoid", bias, 8, 4)
+    bal = epx().balance_loss(l, idx, "sigmoid")
+    d, one = torch.randn((T, K), generator=G.gen(178)).to(DEV), torch.ones(1, device=DEV)
+    dl = epx().route_backward(l, idx, "sigmoid", dtopk_weights=d, balance=bal, dloss=one)
+    i2, w2 = epx().route(off(l), K, "sigmoid", off(bias), 8, 4, out=(off(idx), off(w)))
+    b2 = epx().balance_loss(off(l), i2, "sigmoid",
+                            out=epx().Balance(**{k: off(t) for k, t in vars(bal).items()}))
+    dl2 = epx().route_backward(off(l), i2, "sigmoid", dtopk_weights=off(d), balance=b2,
+                               dloss=off(one), out=off(dl))
+    flags()
+    for a, b in zip([idx, w, dl, *vars(bal).values()], [i2, w2, dl2, *vars(b2).values()]):
+        same(a, b, "unaligned")
+
+
 def test_router_beyond_32_bit_offsets():
     """More than 2^31 logits: a token's results do not depend on where it is."""
     T, E, K, B = (1 << 23) + 5, 264, 3, 4096
