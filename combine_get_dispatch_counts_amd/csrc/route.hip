@@ -174,11 +174,12 @@ __device__ __forceinline__ void shares_of(const float (&l)[N], float (&p)[N], fl
 //
 // Bound by vector instructions, not by memory: 16384 tokens of 256 experts, top-8
 // of the best 4 of 8 groups, sigmoid with a bias (18 MB, 2.6 us at a read's
-// rate) 15.6 us at 1080 instructions a wave, four waves a SIMD. Without the
-// second look it would be 12.4: some ten tokens take it, and a path that few
-// waves run waits for its own instructions as for its data. Softmax without
-// groups or bias 8.4 us. 128 tokens 3.1: one wave's chain of a load, the merges
-// and the weights.
+// rate) 14.4 us at 1080 instructions a wave, four waves a SIMD. Without the
+// second look it would be 12.4: some ten tokens take it, which the others do not
+// hide (it is part of the kernel, since as a function it took its arguments
+// from memory, 0.5 us more; compared through LDS its candidates took another
+// 0.5). Softmax without groups or bias 8.0 us. 128 tokens 3.0: one wave's chain
+// of a load, the merges and the weights.
 
 // Fixed point: B bits for a window below the token's largest key. Keys below
 // the window all have 0, as does what is not live (and what the conversion
@@ -385,10 +386,11 @@ struct Exact {
     const RouteArgs &a;
     const float *row;
     double top, sum;
-    __device__ __forceinline__ Exact(const RouteArgs &args, int64_t t)
+    // scores: keys are scores (else nothing is made of them)
+    __device__ __forceinline__ Exact(const RouteArgs &args, int64_t t, bool scores)
         : a(args), row(args.logits + (size_t)t * args.E), top(0.0), sum(0.0)
     {
-        if constexpr (!SIGMOID) {
+        if (!SIGMOID && scores) {
             float m = -kInf;
             for (int e = lane_id(); e < a.E; e += kWave)
                 m = fmaxf(m, logit(e));
@@ -404,28 +406,23 @@ struct Exact {
         }
     }
     __device__ __forceinline__ float logit(int e) const { return row[e] < kInf ? row[e] : -kInf; }
-    // score and bias, -inf if the expert can not be chosen
-    __device__ __forceinline__ double key(int e) const
+    // score and bias of a logit, -inf if it can not be chosen
+    __device__ __forceinline__ double key(float l, float b) const
     {
-        const double l = (double)logit(e);
-        if (!(l > -(double)kInf))
-            return l;
-        const double s = SIGMOID ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum;
-        if (!a.bias)
-            return s;
-        const float b = a.bias[e];
-        return b < kInf ? s + (double)b : -(double)kInf;
+        const double v = (double)l;
+        const double s = SIGMOID ? 1.0 / (1.0 + exp(-v)) : exp(v - top) / sum;
+        return l > -kInf && l < kInf && b < kInf ? s + (double)b : -(double)kInf;
     }
 };
 
 // One token's groups in 64 bits by the whole wave: bit g for a group that stays.
 template <int N, int L, bool SIGMOID>
-__device__ __noinline__ uint64_t groups64(RouteArgs a, int64_t t, RouteLds<N, L> &lds)
+__device__ __forceinline__ uint64_t groups64(const RouteArgs &a, int64_t t, RouteLds<N, L> &lds)
 {
-    const Exact<SIGMOID> exact(a, t);
+    const Exact<SIGMOID> exact(a, t, true);
     const int lane = lane_id();
     for (int e = lane; e < a.E; e += kWave)
-        lds.key64[e] = exact.key(e);
+        lds.key64[e] = exact.key(exact.row[e], a.bias ? a.bias[e] : 0.0f);
     wave_lds();
     int P = 1;  // lanes of a group
     while (2 * P * a.G <= kWave)
@@ -460,38 +457,50 @@ __device__ __noinline__ uint64_t groups64(RouteArgs a, int64_t t, RouteLds<N, L>
 // One token's choice in 64 bits by the whole wave, among n candidates: chosen[r]
 // is the r-th expert's number, or ~0.
 template <int N, int L, bool SIGMOID>
-__device__ __noinline__ void choose64(RouteArgs a, int64_t t, int n, RouteLds<N, L> &lds,
-                                      uint32_t *chosen)
+__device__ __forceinline__ void choose64(const RouteArgs &a, int64_t t, int n, RouteLds<N, L> &lds,
+                                         uint32_t *chosen)
 {
     const int lane = lane_id();
-    if (a.bias) {
-        const Exact<SIGMOID> exact(a, t);
-        for (int c = lane; c < n; c += kWave)
-            lds.key64[c] = exact.key(lds.candidate[c]);
-    } else {  // the logits order
-        const auto logit = [&](int e) {
-            const float l = a.logits[(size_t)t * a.E + e];
-            return l < kInf ? l : -kInf;
-        };
-        for (int c = lane; c < n; c += kWave)
-            lds.key64[c] = (double)logit(lds.candidate[c]);
-    }
+    const Exact<SIGMOID> exact(a, t, a.bias != nullptr);
+    // a candidate's place in the order (without a bias that of the logits), -inf
+    // if it can not be chosen
+    const auto key = [&](int e) {
+        const float l = exact.row[e];
+        return a.bias ? exact.key(l, a.bias[e]) : l < kInf ? (double)l : -(double)kInf;
+    };
     if (lane < L)
         chosen[lane] = ~0u;
     wave_lds();
-    for (int c = lane; c < n; c += kWave) {
-        const int e = lds.candidate[c];
-        const double k = lds.key64[c];
-        if (!(k > -(double)kInf))  // can not be chosen
-            continue;
+    if (n <= kWave) {  // one each, compared from lane to lane
+        const int e = lane < n ? lds.candidate[lane] : 0;
+        const double k = key(e);
+        const int lo = __double2loint(k), hi = __double2hiint(k);
         int rank = 0;
-#pragma unroll 4
         for (int o = 0; o < n; ++o) {
-            const double ok = lds.key64[o];
-            rank += ok > k || (ok == k && lds.candidate[o] < e);
+            const double ok = __hiloint2double(__builtin_amdgcn_readlane(hi, o),
+                                               __builtin_amdgcn_readlane(lo, o));
+            rank += ok > k || (ok == k && __builtin_amdgcn_readlane(e, o) < e);
         }
-        if (rank < a.K)
+        if (lane < n && k > -(double)kInf && rank < a.K)
             chosen[rank] = (uint32_t)e;
+    } else {
+        for (int c = lane; c < n; c += kWave)
+            lds.key64[c] = key(lds.candidate[c]);
+        wave_lds();
+        for (int c = lane; c < n; c += kWave) {
+            const int e = lds.candidate[c];
+            const double k = lds.key64[c];
+            if (!(k > -(double)kInf))
+                continue;
+            int rank = 0;
+#pragma unroll 4
+            for (int o = 0; o < n; ++o) {
+                const double ok = lds.key64[o];
+                rank += ok > k || (ok == k && lds.candidate[o] < e);
+            }
+            if (rank < a.K)
+                chosen[rank] = (uint32_t)e;
+        }
     }
     wave_lds();
 }
@@ -712,6 +721,8 @@ __global__ __launch_bounds__(kWave, N <= 16 ? 4 : 2) void route_kernel(RouteArgs
                 const bool can = row == q && expert(j) < experts &&
                                  (blind ? a.G == 1 || stays(expert(j)) : w[j] >= from);
                 const uint64_t m = uniform64(__ballot(can));
+                if (!m)
+                    continue;
                 if (can)
                     lds.candidate[n + __builtin_popcountll(m & lanes_below(lane_id()))] =
                         (uint16_t)expert(j);
