@@ -174,7 +174,7 @@ __device__ __forceinline__ void shares_of(const float (&l)[N], float (&p)[N], fl
 //
 // Bound by vector instructions, not by memory: 16384 tokens of 256 experts, top-8
 // of the best 4 of 8 groups, sigmoid with a bias (18 MB, 2.6 us at a read's
-// rate) 14.4 us at 1080 instructions a wave, four waves a SIMD. Without the
+// rate) 14.4 us at 1060 instructions a wave, four waves a SIMD. Without the
 // second look it would be 12.4: some ten tokens take it, which the others do not
 // hide (it is part of the kernel, since as a function it took its arguments
 // from memory, 0.5 us more; compared through LDS its candidates took another
