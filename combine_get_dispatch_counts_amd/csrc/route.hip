@@ -95,10 +95,26 @@ __device__ __forceinline__ float raw_score(float l, float ref)
     }
 }
 
-template <bool SIGMOID>
-__device__ __forceinline__ float score_ref(float top)
+// The logit below which a sigmoid may leave fp32's normal range (it does at
+// -87.3): such a token's scores are taken relative to its largest.
+constexpr float kLowLogit = -80.0f;
+
+// The reference of a token's entries (-inf where there is none): the largest
+// logit; for sigmoids 0, their scores being their own, unless one is low.
+template <bool SIGMOID, int M>
+__device__ __forceinline__ float entry_ref(const float (&l)[M])
 {
-    return SIGMOID ? fminf(top, 0.0f) : top;
+    if constexpr (SIGMOID) {
+        bool low = false;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            low |= l[m] < kLowLogit && l[m] > -kInf;
+        if (!__ballot(low))
+            return 0.0f;
+        const float top = largest(l);
+        return row_ballot(low) ? fminf(top, 0.0f) : 0.0f;
+    }
+    return largest(l);
 }
 
 // A score and its slope (softmax: no factor of its gradient, 1; sigmoid
@@ -110,7 +126,7 @@ __device__ __forceinline__ float entry_score(float l, float ref, float &slope)
         const float t = exp_fp32(-fabsf(l));  // 0 for -inf
         const float r = 1.0f / (1.0f + t), u = t * r;
         slope = l >= 0.0f ? u : r;
-        return ref < -60.0f ? raw_score<true>(l, ref) : l >= 0.0f ? r : u;
+        return ref < 0.0f ? raw_score<true>(l, ref) : l >= 0.0f ? r : u;
     } else {
         slope = 1.0f;
         return l > -kInf ? exp_fp32(l - ref) : 0.0f;
@@ -122,7 +138,7 @@ __device__ __forceinline__ float entry_score(float l, float ref, float &slope)
 template <int N, bool SIGMOID>
 __device__ __forceinline__ void shares_of(const float (&l)[N], float (&p)[N], float *slopes)
 {
-    float top = 0.0f, sum = 0.0f;
+    float sum = 0.0f;
     if constexpr (SIGMOID) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -134,19 +150,30 @@ __device__ __forceinline__ void shares_of(const float (&l)[N], float (&p)[N], fl
             sum += p[j];
         }
         sum = row_sum(sum);
-        // scores that are all near their underflow, relative to the largest
-        if (__ballot(sum < 0x1p-60f)) {
-            top = largest(l);
-            sum = 0.0f;
+        // a share is in fp32's normal range and its score may not be: relative
+        // to the largest, the token's alone, so that none depends on the others
+        // of its wave (above a sum of 1/2 the shares leave the range too)
+        if (__ballot(sum < 0.5f)) {
+            bool low = false;
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                p[j] = raw_score<true>(l[j], score_ref<true>(top));
-                sum += p[j];
+            for (int j = 0; j < N; ++j)
+                low |= l[j] < kLowLogit && l[j] > -kInf;
+            low = row_ballot(low) != 0 && sum < 0.5f;
+            if (__ballot(low)) {
+                const float ref = fminf(largest(l), 0.0f);
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float q = raw_score<true>(l[j], ref);
+                    p[j] = low ? q : p[j];
+                    s += q;
+                }
+                s = row_sum(s);
+                sum = low ? s : sum;
             }
-            sum = row_sum(sum);
         }
     } else {
-        top = largest(l);
+        const float top = largest(l);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             p[j] = exp_fp32(l[j] - top);  // 0 for -inf (and -inf less itself, a NaN)
@@ -743,11 +770,8 @@ __global__ __launch_bounds__(kWave, N <= 16 ? 4 : 2) void route_kernel(RouteArgs
     // weights
     float v[kPer], total = 1.0f;
     if (normalize) {
-        float m = lk[0], sum = 0.0f;
-#pragma unroll
-        for (int q = 1; q < kPer; ++q)
-            m = fmaxf(m, lk[q]);
-        const float ref = score_ref<SIGMOID>(row_max(m));
+        float sum = 0.0f;
+        const float ref = entry_ref<SIGMOID>(lk);
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
             float slope;
@@ -1282,10 +1306,8 @@ __global__ __launch_bounds__(kWave) void route_backward_kernel(RouteBwdArgs a, b
             d[m] = e[m] >= 0 ? d[m] * a.scale : 0.0f;
         }
         if (normalize) {
-            float n[kPer], slopes[kPer], top = lk[0], sum = 0.0f, mean = 0.0f;
-            if (kPer > 1)
-                top = fmaxf(top, lk[kPer - 1]);
-            const float ref = score_ref<SIGMOID>(row_max(top));
+            float n[kPer], slopes[kPer], sum = 0.0f, mean = 0.0f;
+            const float ref = entry_ref<SIGMOID>(lk);
 #pragma unroll
             for (int m = 0; m < kPer; ++m) {
                 n[m] = entry_score<SIGMOID>(lk[m], ref, slopes[m]);

@@ -615,6 +615,57 @@ def test_route_backward_against_differences(scoring):
         assert abs(diff - float(got[t, e])) <= tol, (t, e, diff, float(got[t, e]))
 
 
+def _far_apart(T, E, top, low, seed):
+    """Logits near `low`, of which three a token (experts 0 to 2) are near `top`."""
+    l = low + _logits(T, E, seed, 0.5)
+    l[:, :3] += top - low
+    return l
+
+
+@pytest.mark.parametrize("top,low", [(-59.0, -95.0), (-30.0, -95.0), (-4.0, -89.0), (-59.0, -130.0),
+                                     (-61.0, -95.0), (-75.0, -79.0), (20.0, -95.0)])
+@pytest.mark.parametrize("E,K", [(40, 8), (256, 20)])
+def test_sigmoids_below_their_underflow(top, low, E, K):
+    """Sigmoids that leave fp32's range beside others that do not: normalised weights,
+    shares and their gradients are whole, in both directions."""
+    l = _far_apart(9, E, top, low, 180)
+    l[4] = _logits(1, E, 181)[0]               # an ordinary token beside them
+    _route(l, K, "sigmoid")
+    idx = G.route(l, K, "sigmoid")[0]
+    idx[2] = -1
+    _route_backward(l, idx, "sigmoid", True, 2.5, True, bal=False)
+    _route_backward(l, idx, "sigmoid", True, 2.5, False)
+    _route_backward(l, idx, "sigmoid", True, 2.5, True, [0, 3, 9])
+    keep = [t for t in range(9) if t != 4]     # (it would hide the others' mean shares)
+    _balance(l[keep], idx[keep], "sigmoid")
+
+
+def test_router_results_do_not_depend_on_the_wave():
+    """A token among others of far smaller scores gives the bytes that it gives alone."""
+    E, K = 40, 6
+    l = _far_apart(8, E, -59.0, -95.0, 182)
+    l[5] = -6.0 + _logits(1, E, 183)[0]
+    d = torch.randn((8, K), generator=G.gen(184)).to(DEV)
+    say("route, route_backward, balance_loss of one token, alone and among others")
+    idx, w = epx().route(gpu(l), K, "sigmoid")
+    one = torch.ones(1, device=DEV)
+    off = torch.arange(9, dtype=torch.int32, device=DEV)
+    b = epx().balance_loss(gpu(l), idx, "sigmoid", off)
+    dl = epx().route_backward(gpu(l), idx, "sigmoid", dtopk_weights=d, balance=b, dloss=one * 8,
+                              seq_off=off)
+    for n in (1, 4):                           # four are a wave of it
+        l1, off1 = gpu(l[5:6].repeat(n, 1)), off[:n + 1]
+        i1, w1 = epx().route(l1, K, "sigmoid")
+        b1 = epx().balance_loss(l1, i1, "sigmoid", off1)
+        d1 = epx().route_backward(l1, i1, "sigmoid", dtopk_weights=d[5:6].repeat(n, 1), balance=b1,
+                                  dloss=one * n, seq_off=off1)
+        flags()
+        for a, c, what in ((idx[5:6], i1, "idx"), (w[5:6], w1, "weights"),
+                           (b.probs[5:6], b1.probs, "shares"), (dl[5:6], d1, "gradient")):
+            for row in c:
+                same(a[0], row, what)
+
+
 # -------------------------------------------------------- combine's gradient
 
 @pytest.mark.parametrize("T,h,K", [(1, 8, 1), (5, 128, 2), (9, 1032, 3), (4, 2056, 9), (6, 4096, 6),
