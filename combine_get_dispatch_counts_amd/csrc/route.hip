@@ -356,9 +356,11 @@ __device__ __forceinline__ void best_two(float &x, float &y, float ox, float oy)
     x = fmaxf(x, ox);
 }
 
-// Bits of the groups that stay, at (group << shift); near: a kept and a dropped
-// group's scores are within tol of each other. 2^shift lanes of a token walk a
-// group (one with more than 16 groups, when a lane has several).
+// Bits of the groups that stay, at (group << shift); near: half of a kept and
+// of a dropped group's scores are within tol of each other (halves, because
+// two keys of the type's largest or lowest value have no sum in fp32).
+// 2^shift lanes of a token walk a group (one with more than 16 groups, when a
+// lane has several).
 template <int N, int L>
 __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, RouteLds<N, L> &lds, int shift,
                                                 bool fours, float tol, bool &near)
@@ -383,7 +385,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, RouteLds<N, 
         for (int d = 1; d < P; d <<= 1)
             best_two(x, y, __shfl_xor(x, d, kWave), __shfl_xor(y, d, kWave));
         if (part == 0)
-            score[g] = y > -kInf ? x + y : x;
+            score[g] = y > -kInf ? 0.5f * x + 0.5f * y : 0.5f * x;
     }
     wave_lds();
     uint64_t bits = 0;
@@ -638,8 +640,8 @@ __global__ __launch_bounds__(kWave, N <= 16 ? 4 : 2) void route_kernel(RouteArgs
                     unit[RouteLds<N, L>::at(expert(j))] = key[j];
             }
             wave_lds();
-            // a score is two keys and a rounding
-            kept = best_groups<N, L>(a, lds, shift, fours, 3.0f * pair, near);
+            // half a score is two halves of a key and a rounding
+            kept = best_groups<N, L>(a, lds, shift, fours, 1.5f * pair, near);
             const uint64_t unsure = uniform64(__ballot(near && live));
 #pragma unroll 1
             for (int q = 0; unsure && q < kTokens; ++q) {

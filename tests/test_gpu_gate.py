@@ -371,6 +371,30 @@ def test_route_mask_and_rows():
     flags()
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G_", [(64, 8), (72, 8), (256, 64), (12, 3), (96, 3)])
+def test_route_groups_of_largest_and_lowest_biases(scoring, E, G_):
+    """Biases at the ends of fp32's range, whose sums of two are beyond it: groups
+    that are masked by the lowest value are live and come in their order, those of
+    the largest are told apart."""
+    least, most, per = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max, E // G_
+    l = _logits(11, E, 185)
+    bias = torch.full((E,), least)
+    bias[2 * per:3 * per] = 0.0                # one group; the others follow, lowest first
+    _route(l, min(per + 3, 32), scoring, bias, G_, min(3, G_))
+    bias[2 * per:3 * per] = least              # nothing but masks
+    _route(l, 2, scoring, bias, G_, 2)
+    bias = torch.zeros(E)
+    bias[0:per] = 0.7 * most                   # twice 0.7 against 1 + 0.5 and 0.6 + 0.6
+    bias[per], bias[per + 1] = most, 0.5 * most
+    bias[2 * per:2 * per + 2] = 0.6 * most
+    _route(l, 2, scoring, bias, G_, 1)
+    _route(l, 4, scoring, bias, G_, 2)
+    bias[:] = -torch.inf                       # one live expert in a group: it alone
+    bias[per - 1], bias[per], bias[per + 1] = least, least, least
+    _route(l, 3, scoring, bias, G_, 1)
+
+
 # ---------------------------------------------------------- balance loss
 
 def _choose(T, E, K, seed, drop=0.1):
