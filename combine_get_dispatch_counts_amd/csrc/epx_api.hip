@@ -1006,7 +1006,8 @@ int epx_combine_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *exp
     if ((rc = check_hidden(h, 0)) != EPX_OK)
         return rc;
     if (T > 0) {
-        if (!dout || !topk_w || !pos || (!d_expert_out && !d_topk_w) ||
+        // (a buffer of no rows has no address)
+        if (!dout || !topk_w || !pos || (n_rows > 0 && !d_expert_out && !d_topk_w) ||
             (n_rows > 0 && d_topk_w && !expert_out))
             return EPX_EINVAL;
         if (!aligned16(dout) || !aligned16(expert_out) || !aligned16(d_expert_out))

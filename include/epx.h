@@ -663,9 +663,10 @@ int epx_route_backward(epx_ctx *ctx, const float *logits, const int64_t *topk_id
  *      dout[t], rounded once; rows that no entry names are left as they were.
  *      d_topk_w [T, K] fp32, or NULL (expert_out may then be NULL too): the
  *      sum over the channels of dout[t] * expert_out[pos[t,k]] in fp32, in a
- *      fixed order; 0 where pos < 0. At least one of the two. A handle row >=
- *      n_rows sets EPX_DEV_BAD_HANDLE and counts as -1. Buffers of rows
- *      16-byte aligned; outputs must not overlap inputs. */
+ *      fixed order; 0 where pos < 0. At least one of the two (with n_rows = 0
+ *      both may be NULL). A handle row >= n_rows sets EPX_DEV_BAD_HANDLE and
+ *      counts as -1. Buffers of rows 16-byte aligned; outputs must not overlap
+ *      inputs. */
 int epx_combine_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *expert_out,
                          int64_t n_rows, int h, const float *topk_w, const int32_t *pos, int T,
                          int K, uint16_t *d_expert_out, float *d_topk_w, hipStream_t stream);

@@ -757,6 +757,24 @@ def test_combine_backward_bad_handle():
     flags()
 
 
+@pytest.mark.parametrize("h", [64, 520])
+def test_combine_backward_no_expert_rows(h):
+    """No expert rows at all, each gradient alone and both."""
+    dout, w = gpu(G.rows((3, h), 186), torch.rand((3, 2)))
+    none = torch.full((3, 2), -1, dtype=torch.int32, device=DEV)
+    y = torch.empty((0, h), dtype=torch.bfloat16, device=DEV)
+    say(f"combine_backward of no rows h={h}")
+    dy, _ = epx().combine_backward(dout, None, none, w, out=(y, None))
+    assert dy.shape == (0, h)
+    _, dw = epx().combine_backward(dout, y, none, w, out=(None, torch.ones_like(w)))
+    assert not dw.any()
+    dy, dw = epx().combine_backward(dout, y, none, w)
+    assert dy.shape == (0, h) and not dw.any()
+    flags()
+    epx().combine_backward(dout, None, none + 1, w, out=(y, None))
+    flags(4)
+
+
 # ------------------------------------------------------------ as they are used
 
 def _step(x, r, wn, wr, w13, w2, K, off, dnext, dtop_stream):
