@@ -6,9 +6,10 @@
 // holds the token's row in registers (its other waves find it in the cache),
 // reads the entry's expert row once, stores the scaled row and sums the
 // products over the wave. HBM-bound: per entry one row read and one written
-// (4096 tokens of top-8 x 7168, 1 GB: 170-174 us, 5.8 TB/s). Few tokens are
-// bound by the wave that has an entry, its loads and then its stores: 16 tokens
-// 7.4 us, 128 10.3, 512 25.1 (5.0 TB/s).
+// (4096 tokens of top-8 x 7168, 1 GB: 172-177 us, 5.7 TB/s). Few tokens are
+// bound by the wave that has an entry, its loads and then its stores, and by
+// the compute units without a block: 16 tokens 6.2 us, 128 9.9, 512 22.5 (5.5
+// TB/s).
 #include "gate_device.h"
 
 namespace epx {
@@ -133,14 +134,14 @@ hipError_t launch_narrow(const CombineBwdArgs &a, hipStream_t stream)
 
 // With many rows the sums and the scaled rows take a launch each: the token's
 // row is read twice, but memory reads alone and then writes alone. One against
-// two launches, top-8, h = 7168: 256 tokens (28 MB of expert rows) 12.4 / 13.3
-// us, 512 25.6 / 24.5, 1024 51 / 46.5, 4096 194 / 170-174, 8192 385 / 337; h =
-// 2048, 4096 tokens 57 / 52; top-6 x 4096, 4096 tokens 80 / 74.5. Where the
+// two launches, top-8, h = 7168: 256 tokens (28 MB of expert rows) 12.2 / 11.9
+// us, 512 23.4 / 22.4, 1024 49 / 45, 4096 202 / 172-177, 8192 376 / 332; h =
+// 2048, 4096 tokens 58 / 52.5; top-6 x 4096, 4096 tokens 85 / 79. Where the
 // token's row is a larger part, or rows are short, one launch: 8192 tokens of
-// top-2 x 4096 55 / 64, of top-4 x 2048 51 / 53, of top-8 x 1024 52 / 56. (Rows
-// written in their own order by a second launch that finds each one's token,
-// which is sequential for memory but reads the tokens' rows eight times past
-// the L2: 221 us for 4096 tokens of top-8 x 7168.)
+// top-2 x 4096 53-55 / 62, of top-4 x 2048 51-55 / 53, of top-8 x 1024 52-58 /
+// 57-62. (Rows written in their own order by a second launch that finds each
+// one's token, which is sequential for memory but reads the tokens' rows eight
+// times past the L2: 221 us for 4096 tokens of top-8 x 7168.)
 bool split(const CombineBwdArgs &a)
 {
     return a.dy && a.dtopk_w && a.K >= 6 && a.h >= 2048 &&
@@ -165,6 +166,14 @@ hipError_t launch(const CombineBwdArgs &a, hipStream_t stream)
 
 }  // namespace
 
+// A step takes 1, 4 or 8 vectors of a lane, the least that hold the row, or 8
+// where none does. With 1 / 4 / 8 of them 4096 tokens of top-8 take at 512
+// channels 15.2 / 22.2 / 33.5 us, 1024 26.6 / 28.6 / 41, 2048 54 / 51 / 60, 4096
+// 100 / 97.5 / 97, 7168 171 / 172 / 171; 64 tokens at 512 channels 2.1 / 2.7 /
+// 3.4, 2048 3.0 / 3.2 / 3.8, 4096 5.2 / 4.7 / 4.7, 7168 11.1 / 9.3 / 8.0. More
+// vectors leave fewer waves a SIMD and longer rows a second step that is mostly
+// empty: 14 against 8, 4096 tokens of 5120 channels 133 / 128.5, 7168 174 / 174,
+// 8192 209 / 191; 128 tokens 7.5 / 8.3, 9.9 / 9.9 and 13.7 / 11.
 static hipError_t launch_tokens(const CombineBwdArgs &a, hipStream_t stream)
 {
     if (a.h <= 128)
@@ -175,9 +184,7 @@ static hipError_t launch_tokens(const CombineBwdArgs &a, hipStream_t stream)
         return launch<1>(a, stream);
     if (a.h <= 2048)
         return launch<4>(a, stream);
-    if (a.h <= 4096)
-        return launch<8>(a, stream);
-    return launch<14>(a, stream);
+    return launch<8>(a, stream);
 }
 
 hipError_t launch_combine_backward(const CombineBwdArgs &args, hipStream_t stream)

@@ -741,6 +741,22 @@ def test_combine_backward_more_tokens_than_a_launch(T, h, K):
             assert bool(((dw[t, k].double() - x.sum(1)).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("h", [8192, 8200, 12296])
+def test_combine_backward_long_rows_in_two_launches(h):
+    """Rows of one step and more, whole and in part, sums and scaled rows a launch each."""
+    T, K = 600, 6
+    dout, y = G.rows((T, h), 204), G.rows((T * K, h), 205)
+    w = torch.rand((T, K), generator=G.gen(206))
+    pos = torch.randperm(T * K, generator=G.gen(207)).to(torch.int32).view(T, K)
+    say(f"combine_backward T={T} h={h} K={K}")
+    dy, dw = epx().combine_backward(gpu(dout), gpu(y), gpu(pos), gpu(w))
+    flags()
+    ref, named, rw, tol = G.combine_backward(dout, y, pos, w)
+    assert named.all()
+    same(dy.cpu(), ref, "d_expert_out")
+    X.assert_close(dw, rw, tol, "d_topk_weights")
+
+
 def test_combine_backward_bad_handle():
     dout, y, w = gpu(G.rows((3, 64), 144), G.rows((4, 64), 145), torch.rand((3, 2)))
     pos = torch.tensor([[0, 4], [-7, 1], [3, 2]], dtype=torch.int32)
