@@ -431,6 +431,8 @@ __global__ __launch_bounds__(kNarrowThreads) void norm_narrow_backward_kernel(No
         for (int q = 0; q < kNarrowSteps; ++q) {
             const int64_t t = t0 + q * step;
             live[q] = t < a.T && i < nvec;
+            // (what a lane without a row or channels reads it does not use; in
+            // place it may be another row's gradient already)
             at[q] = (size_t)(live[q] ? t * a.h + i * 8 : 0);
             x[q] = load16_stream(a.x + at[q]);
             d[q] = load16_stream(a.dout + at[q]);

@@ -224,6 +224,34 @@ def test_norm_backward_in_place_and_empty():
     flags()
 
 
+@pytest.mark.parametrize("h", [8, 64, 128, 200, 256])
+@pytest.mark.parametrize("T", [1, 33, 2601])
+def test_norm_in_place_narrow(h, T):
+    """Rows that go several to a wave, over their own inputs, forward and backward."""
+    m = epx()
+    x, r, s, w = gpu(G.rows((T, h), 191), G.rows((T, h), 192), G.rows((T, h), 193),
+                     1 + 0.1 * torch.randn(h, generator=G.gen(194)))
+    say(f"rms_norm and its gradient in place T={T} h={h}")
+    want = m.rms_norm(x, w, residual=r)
+    for swap in (False, True):                 # the sum over the residual or over x
+        a, b = x.clone(), r.clone()
+        to = m.Normed(out=b, residual=a) if swap else m.Normed(out=a, residual=b)
+        m.rms_norm(a, w, residual=b, buf=to)
+        same(to.out, want.out, "out")
+        same(to.residual, want.residual, "residual")
+    a = x.clone()
+    m.rms_norm(a, w, buf=m.Normed(out=a))
+    same(a, m.rms_norm(x, w).out, "out alone")
+    dx, dw = m.rms_norm_backward(r, x, w, dresidual=s)
+    for over in (0, 1):
+        a, b = r.clone(), s.clone()
+        out = (b if over else a, torch.empty_like(dw))
+        m.rms_norm_backward(a, x, w, dresidual=b, out=out)
+        same(out[0], dx, "dx")
+        same(out[1], dw, "dweight")
+    flags()
+
+
 # ---------------------------------------------------------------- router
 
 def _logits(T, E, seed, scale=1.5):
@@ -393,6 +421,29 @@ def test_route_groups_of_largest_and_lowest_biases(scoring, E, G_):
     bias[:] = -torch.inf                       # one live expert in a group: it alone
     bias[per - 1], bias[per], bias[per + 1] = least, least, least
     _route(l, 3, scoring, bias, G_, 1)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [-100.0, -1e9, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("G_,top", [(1, 1), (8, 3)])
+def test_route_finite_masks(scoring, mask, G_, top):
+    """Experts masked by a finite bias: last, not out."""
+    E = 64
+    l, bias = _logits(21, E, 187), torch.zeros(E)
+    bias[torch.randperm(E, generator=G.gen(188))[:20]] = mask
+    _route(l, 8, scoring, bias, G_, top)
+    bias[8:] = mask                            # fewer than K without a mask
+    _route(l, 12, scoring, bias, G_, top)
+
+
+@pytest.mark.parametrize("scale", [1e-4, 25.0, 300.0])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_narrow_and_wide_logits(scoring, scale):
+    """Logits nearer than the fixed point tells, and chosen ones outside its window."""
+    l = _logits(40, 256, 189, scale)
+    _route(l, 8, scoring)
+    _route(l, 16, scoring, normalize=False)
+    _route(l, 8, scoring, torch.randn(256, generator=G.gen(190)) * 0.1, 8, 4)
 
 
 # ---------------------------------------------------------- balance loss
@@ -864,6 +915,36 @@ def test_step_against_differentiation():
     assert rel(s["dwn"], w.grad) < 2.0 ** -5
 
 
+def test_norm_fp8_rows_reach_the_products():
+    """The normed FP8 rows through an expert that every token visits: what the
+    quantised weights make of them, beside 64 bits from the same codes."""
+    m = epx()
+    T, h, f = 130, 512, 256
+    x, r = G.rows((T, h), 195), G.rows((T, h), 196, 3.0)
+    wn = (1 + 0.1 * torch.randn(h, generator=G.gen(197))).to(torch.bfloat16)
+    w13, w2 = G.rows((1, 2 * f, h), 198, h ** -0.5), G.rows((1, h, f), 199, f ** -0.5)
+    say("rms_norm's FP8 rows through grouped_swiglu and grouped_gemm")
+    n = m.rms_norm(gpu(x), gpu(wn), residual=gpu(r), fp8=True)
+    q13, s13 = m.quantize_weights(gpu(w13))
+    q2, s2 = m.quantize_weights(gpu(w2))
+    off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    up = m.grouped_gemm(n.codes, q13, off, n.scales, s13)
+    act, act_s = m.grouped_swiglu(n.codes, q13, off, n.scales, s13)
+    y = m.grouped_gemm(act, q2, off, act_s, s2)
+    flags()
+    rows, w64 = X.rows64(n.codes.cpu(), n.scales.cpu()), X.weights64(q13[0].cpu(), s13[0].cpu())
+    want, tol = X.product(rows, w64)
+    tol = tol + X.cut(n.codes.cpu(), n.scales.cpu(), q13[0].cpu(), s13[0].cpu())
+    X.assert_close(up, want, tol + X.BF16 * (want.abs() + tol), "product")
+    # through both products, beside the layer from the unrounded normed rows: four
+    # roundings to e4m3, 2^-4 each at most, which add in squares
+    v = x.double() + r.double()
+    v, _ = G.norm(v, wn.double(), 1e-6)
+    g, u = (v @ w13[0].double().T).split(f, 1)
+    ref = (torch.nn.functional.silu(g) * u) @ w2[0].double().T
+    assert float((y.cpu().double() - ref).norm() / ref.norm()) <= 2.0 ** -3
+
+
 def _flat(s):
     return [t for t in (s["n"].out, s["n"].residual, s["idx"], s["top"], s["bal"].loss,
                         s["bal"].counts, s["bal"].probs, s["bal"].num_tokens, s["out"], s["dy"],
@@ -901,6 +982,27 @@ def test_step_is_repeatable_and_replays():
         flags()
         for a, b in zip(held, ref):
             same(a, b, f"replay {replay}")
+
+
+def test_dispatch_gradient_is_a_combine():
+    """A token's row goes to each of its entries' rows, so the gradient that comes
+    back is their sum: a combine with weights of one."""
+    m = epx()
+    T, h, E, K = 90, 264, 16, 4
+    idx = _choose(T, E, K, 200)
+    x, dr = G.rows((T, h), 201), G.rows((int((idx >= 0).sum()), h), 202)
+    w = torch.rand((T, K), generator=G.gen(203))
+    say("dispatch's gradient")
+    d = m.dispatch(gpu(x), gpu(idx), gpu(w), E, 1)
+    got = m.combine(gpu(dr), d.pos_exp, torch.ones((T, K), device=DEV))
+    flags()
+    same(d.recv_x.cpu(), x[d.recv_src.cpu().long()], "recv_x")
+    v = x.double().requires_grad_()
+    (v[d.recv_src.cpu().long()] * dr.double()).sum().backward()
+    # K terms in fp32, then bf16
+    mag = torch.zeros((T, h)).double().index_add_(0, d.recv_src.cpu().long(), dr.double().abs())
+    tol = K * G.U * mag
+    X.assert_close(got, v.grad, tol + G.BF16 * (v.grad.abs() + tol), "dx")
 
 
 def _repeated(base, T):
