@@ -8,6 +8,11 @@ HIP stream, and marshals pointers and sizes. Names follow the C ABI
 Shapes: x [T,h] bf16; topk_idx [T,K] int64 (-1 = no route); topk_weights
 [T,K] fp32. Destination ranks are logical partitions of the experts:
 rank r holds experts [r*L, (r+1)*L), L = num_experts // num_ranks.
+
+No call takes part in autograd: tensors that require a gradient are read like
+others, and outputs have no history. The gradients are calls of their own
+(rms_norm_backward, route_backward, combine_backward); dispatch's is a combine
+of the rows' gradient with weights of one.
 """
 from __future__ import annotations
 
@@ -848,7 +853,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     alone without one), x and residual [T,h] bf16, weight [h] bf16 or fp32.
     Returns v in bf16 (``residual``, where one was given), y in bf16 (``out``,
     with ``bf16``) and y as FP8 rows in dispatch's format (``codes`` and
-    ``scales``, with ``fp8``), what grouped_gemm and grouped_swiglu read. ``buf``
+    ``scales``, with ``fp8``), what grouped_gemm and grouped_swiglu read for an
+    expert that every token visits (dispatch takes bf16 rows). ``buf``
     (alloc_norm's, or any tensors of those shapes) avoids allocating and says
     by its members which outputs there are; its residual may be ``residual``
     or ``x`` itself, and its out one of them that its residual is not."""
@@ -944,7 +950,8 @@ def route(logits: torch.Tensor, topk: int, scoring: str = "softmax",
     scores, over their sum with ``normalize``, times ``scale``. With
     ``num_groups`` > 1 only the experts of the ``topk_groups`` best groups
     (sum of the two best) can be chosen. A logit of -inf keeps an expert
-    from being chosen; ``mask`` [T] bool (or uint8) is False for padding,
+    from being chosen, and a bias of -inf keeps it from all tokens (a large
+    finite one only puts it last, and slows the call); ``mask`` [T] bool (or uint8) is False for padding,
     which gets -1 and 0 everywhere, as entries do for which no expert is
     left. ``out`` (topk_idx, topk_weights) avoids allocating."""
     dev, T, E = _rows(logits, torch.float32, "logits")

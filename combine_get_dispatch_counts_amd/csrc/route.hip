@@ -189,8 +189,8 @@ __device__ __forceinline__ void shares_of(const float (&l)[N], float (&p)[N], fl
 
 // ------------------------------------------------------------------- choice
 //
-// The choice is that of the exact scores. It is made on whole numbers that
-// rise with the keys (score + bias; without a bias the logits themselves): a
+// The choice is that of the scores in 64 bits (without a bias that of the
+// logits). It is made on whole numbers that rise with the keys (score + bias; without a bias the logits themselves): a
 // key's distance from the token's largest in fixed point, with the expert's
 // number below it, so that one unsigned maximum or minimum moves both and
 // equal keys order by their experts. Each lane sorts its experts in such

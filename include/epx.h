@@ -549,8 +549,10 @@ int epx_moe_decode(epx_ctx *ctx, const uint16_t *x, int h, const int64_t *topk_i
  * Out: residual_out [T, h] bf16 = v (with a residual; else NULL); out [T, h]
  *      bf16 = y, or NULL; codes [T, h] and scales [T, epx_scale_stride(h)] =
  *      y as FP8 rows in epx_dispatch's format (s = max(amax, 1e-4) / 448 per
- *      128 channels, code e4m3(y / s), padding +0), or both NULL. At least one
- *      of out and codes. Every output is rounded once from fp32: y is not made
+ *      128 channels, code e4m3(y / s), padding +0), as epx_grouped_gemm and
+ *      epx_grouped_swiglu read them for an expert that every token visits
+ *      (epx_dispatch takes bf16 rows), or both NULL. At least one of out and
+ *      codes. Every output is rounded once from fp32: y is not made
  *      from the rounded v, nor the codes from the rounded y.
  * h a multiple of 8, with codes of 128 (else EPX_EUNSUPPORTED), at most
  * EPX_MAX_NORM_CHANNELS. Buffers 16-byte aligned. residual_out may be residual or
@@ -605,8 +607,13 @@ int epx_rms_norm_backward(epx_ctx *ctx, const uint16_t *dout, const uint16_t *x,
  *      token's chosen with `normalize`; 0 beside a -1. As epx_dispatch,
  *      epx_moe_decode and epx_combine read them.
  * Scores are in fp32 with full relative precision down to their underflow;
- * normalized weights also below it. The choice is that of the exact scores of
- * the given logits, computed again in 64 bits where fp32 cannot tell. K <= E,
+ * normalized weights also below it. Without a bias the order is that of the
+ * logits; with one, and for groups, that of s_e + bias_e in 64 bits, made again
+ * so where fp32 cannot tell (experts that 64 bits cannot tell tie: beside a
+ * bias of -1e9 scores count to 1e-7, beside the lowest fp32 value not at all).
+ * Tokens that are done again take longer: all of them where a finite bias is
+ * of large magnitude (mask with -inf), those whose K-th logit is 32 or more
+ * below their largest, and those with fewer than K experts. K <= E,
  * K <= EPX_MAX_TOPK, E <= EPX_MAX_EXPERTS, T <= EPX_MAX_ROUTER_TOKENS. */
 int epx_route(epx_ctx *ctx, const float *logits, const float *bias, const uint8_t *mask, int T,
               int E, int K, int scoring, int num_groups, int topk_groups, int normalize,
@@ -659,6 +666,8 @@ int epx_route_backward(epx_ctx *ctx, const float *logits, const int64_t *topk_id
  * In:  dout [T, h] bf16; expert_out [n_rows, h] bf16, topk_w [T, K] fp32 and
  *      pos [T, K] as given to epx_combine (no row named twice, as in every
  *      handle).
+ * (The dispatch's gradient is an epx_combine of the rows' gradient with weights
+ * of one.)
  * Out: d_expert_out [n_rows, h] bf16, or NULL: row pos[t,k] = topk_w[t,k] *
  *      dout[t], rounded once; rows that no entry names are left as they were.
  *      d_topk_w [T, K] fp32, or NULL (expert_out may then be NULL too): the
